@@ -445,6 +445,130 @@ quest_status quest_dequantize_sparse24(const uint8_t* codes, const uint8_t* inde
 size_t quest_sparse24_codes_bytes(int64_t rows, int64_t cols, int b);
 size_t quest_sparse24_index_bytes(int64_t rows, int64_t cols);
 
+/*
+ * The feed-forward half of a decoder layer around the quantised products:
+ * activation checkpoints in 8 bits, layer norm and the gated product.  The
+ * pages train Llama-family models with the quantiser on the inputs and weights
+ * of every linear layer (pith.science review of QuEST, "What carries the
+ * argument"); these are the operators between those products.  They take any
+ * number of columns (no multiple is needed except where said).
+ */
+
+/*
+ * Activation checkpoints in 8 bits: what a training step keeps of an
+ * activation for its backward pass, at 8.25 bits an entry.
+ *   Each row is cut into blocks of 32 columns, the last possibly shorter.  E is
+ *   the biased fp32 exponent of a block's largest magnitude (0 for zeros and
+ *   fp32 subnormals), one byte a block; an entry x is held as
+ *     q = clamp(round(x * 2^(133 - E)), -127, 127)   (ties to even),
+ *   one byte, and stands for q * 2^(E - 133).  This is the OCP Microscaling
+ *   Formats specification v1.0's MXINT8 (E8M0 scale, blocks of 32, value
+ *   q / 64 * 2^(E - 127)).  Values are exact in bf16 and fp32; the error is at
+ *   most 2^-7 of the block's largest magnitude (2^-6 for the few entries that
+ *   the clamp takes from 128 to 127 steps).
+ *   A block that holds an infinity or NaN has E = 255 and codes 0, and stands
+ *   for NaN in every entry.
+ *   codes  rows x cols bytes, row-major
+ *   scale  rows x ceil(cols / 32) bytes (quest_act8_scale_bytes)
+ */
+size_t quest_act8_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Save x (rows x cols, 1 <= cols <= 2^20, rows * cols at most 2^36)
+ * and read it back as out_dtype.  Pointers 16-byte aligned; no output may
+ * overlap another argument (QUEST_EINVAL).  Infinities and NaN are allowed.
+ */
+quest_status quest_act8_save(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, int8_t* codes,
+                             uint8_t* scale, void* stream);
+quest_status quest_act8_load(const int8_t* codes, const uint8_t* scale, int64_t rows, int64_t cols, void* out,
+                             quest_dtype out_dtype, void* stream);
+
+/*
+ * Layer norm of each row of x (rows x cols):
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   xhat = (x - mean) rstd,  y = xhat * weight + bias,
+ * in fp32, rounded once to x_dtype.
+ *   weight, bias  cols entries of param_dtype each, or NULL (1 and 0); param_dtype
+ *                 is checked only when one of them is given
+ *   eps           > 0 and finite, also as an fp32 number
+ *   y             rows x cols of x_dtype
+ *   mean, rstd    rows floats each, or NULL (not written)
+ *   codes, scale  the 8-bit checkpoint of xhat (rounded from fp32) for
+ *                 quest_layer_norm_bwd, or both NULL
+ * 1 <= cols <= QUEST_MAX_COLS; rows, alignment and overlaps as for
+ * quest_act8_save.  Infinities and NaN
+ * stay within their row; a row's sum of squares about its mean must be finite
+ * in fp32.
+ */
+quest_status quest_layer_norm_fwd(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, const void* weight,
+                                  const void* bias, quest_dtype param_dtype, double eps, void* y, float* mean,
+                                  float* rstd, int8_t* codes, uint8_t* scale, void* stream);
+
+/*
+ * Its backward pass.  With a = dy * weight (dy without a weight):
+ *   dx = rstd * (a - mean_c a - xhat * mean_c(a * xhat)),
+ *   dweight = sum_r dy * xhat,  dbias = sum_r dy.
+ *   dy, x, dx      rows x cols of dtype
+ *   x, mean        the forward's input and mean; or both NULL and
+ *   codes, scale   the forward's checkpoint, whose values are then xhat (both
+ *                  NULL otherwise)
+ *   rstd           rows floats from the forward
+ *   dx             or NULL (not written)
+ *   dweight, dbias cols entries of param_dtype each, or NULL (not written);
+ *                  param_dtype is checked when weight, dweight or dbias is given
+ *   workspace      device, quest_layer_norm_workspace_bytes(rows, cols) bytes,
+ *                  written; may be NULL if dweight and dbias are.  Calls that
+ *                  can run at the same time need one each.
+ * The sums over rows are added in an order that rows and cols fix.  With
+ * rows == 0, dweight and dbias are set to zero.  At least one of dx, dweight
+ * and dbias is needed (QUEST_EINVAL).  No output may overlap another argument.
+ */
+size_t quest_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+quest_status quest_layer_norm_bwd(const void* dy, quest_dtype dtype, int64_t rows, int64_t cols, const void* x,
+                                  const float* mean, const int8_t* codes, const uint8_t* scale, const float* rstd,
+                                  const void* weight, quest_dtype param_dtype, void* dx, void* dweight, void* dbias,
+                                  void* workspace, void* stream);
+
+/* Activations of the gated product: g / (1 + exp(-g)), and g * Phi(g) with the
+   standard normal distribution function Phi. */
+typedef enum { QUEST_SILU = 0, QUEST_GELU = 1, QUEST_ACT_INT_RANGE_ = 0x7FFFFFFF } quest_act;
+
+/*
+ * Gated product of quantised operands:
+ *   g = Q(X) Q(gate)^T,  u = Q(X) Q(up)^T  (n x m, each as quest_gemm's product),
+ *   out = act(g) * u,
+ * with one rounding, to out_dtype, after g and u (which are rounded as
+ * quest_gemm's fp32 output).
+ *   x, x_scale        operand of n rows and k columns, x_bits, as for quest_gemm
+ *   gate, up          operands of m rows and k columns, w_bits, with their
+ *                     clip scales gate_scale and up_scale
+ *   m, n, k           0 <= m <= 2^20, 0 <= n <= 2^30, k as for quest_gemm, and
+ *                     at most 2^23 - 1 tiles of 256 x 128 (QUEST_EUNSUPPORTED)
+ *   out               n x m row-major elements of out_dtype
+ *   gate_codes, gate_exp, up_codes, up_exp
+ *                     the 8-bit checkpoints of g and u (codes n x m, exponents
+ *                     n x ceil(m / 32) bytes), all four or none (NULL)
+ * All pointers 16-byte aligned (QUEST_EALIGN); no output may overlap another
+ * argument (QUEST_EINVAL).  gate and up may be the same buffer.
+ */
+quest_status quest_gated_fwd(const uint8_t* x, const float* x_scale, int64_t n, int x_bits, const uint8_t* gate,
+                             const float* gate_scale, const uint8_t* up, const float* up_scale, int64_t m, int w_bits,
+                             int64_t k, quest_act act, void* out, quest_dtype out_dtype, int8_t* gate_codes,
+                             uint8_t* gate_exp, int8_t* up_codes, uint8_t* up_exp, void* stream);
+
+/*
+ * Its backward pass from the checkpoints' values g and u:
+ *   out[:, :cols] = dh * u * act'(g)   (gradient reaching g),
+ *   out[:, cols:] = dh * act(g)        (gradient reaching u),
+ * rows x 2 cols row-major of dtype: the left operand of the products that give
+ * the gradients of x (with [Q(gate); Q(up)]) and of both weights.
+ *   dh    rows x cols of dtype;  0 <= cols <= 2^20, rows * cols at most 2^36
+ * Alignment and overlaps as for quest_gated_fwd.
+ */
+quest_status quest_gated_bwd(const void* dh, quest_dtype dtype, int64_t rows, int64_t cols, const int8_t* gate_codes,
+                             const uint8_t* gate_exp, const int8_t* up_codes, const uint8_t* up_exp, quest_act act,
+                             void* out, void* stream);
+
 /* Bytes of the packed codes: rows * cols * b / 8 (0 on invalid sizes). */
 size_t quest_codes_bytes(int64_t rows, int64_t cols, int b);
 

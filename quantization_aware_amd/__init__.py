@@ -35,6 +35,12 @@ __all__ = [
     "dequantize_sparse24",
     "dequantize",
     "trust_bwd",
+    "act8_save",
+    "act8_load",
+    "layer_norm_fwd",
+    "layer_norm_bwd",
+    "gated_fwd",
+    "gated_bwd",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -44,6 +50,7 @@ LIB_PATH = os.environ.get("QUEST_LIBRARY") or os.path.join(os.path.dirname(os.pa
 
 QUEST_OK, QUEST_EINVAL, QUEST_EUNSUPPORTED, QUEST_EALIGN, QUEST_EHIP = range(5)
 QUEST_F32, QUEST_BF16 = 0, 1
+ACTIVATIONS = {"silu": 0, "gelu": 1}  # quest_act
 
 EXPORTED_SYMBOLS = (
     "quest_fit_alpha",
@@ -67,6 +74,14 @@ EXPORTED_SYMBOLS = (
     "quest_trust_bwd",
     "quest_codes_bytes",
     "quest_mask_bytes",
+    "quest_act8_scale_bytes",
+    "quest_act8_save",
+    "quest_act8_load",
+    "quest_layer_norm_fwd",
+    "quest_layer_norm_workspace_bytes",
+    "quest_layer_norm_bwd",
+    "quest_gated_fwd",
+    "quest_gated_bwd",
     "quest_status_string",
 )
 
@@ -153,6 +168,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.quest_codes_bytes.restype = ctypes.c_size_t
     lib.quest_mask_bytes.argtypes = [i64, i64]
     lib.quest_mask_bytes.restype = ctypes.c_size_t
+    lib.quest_act8_scale_bytes.argtypes = [i64, i64]
+    lib.quest_act8_scale_bytes.restype = ctypes.c_size_t
+    lib.quest_act8_save.argtypes = [vp, c_int, i64, i64, vp, vp, vp]
+    lib.quest_act8_save.restype = c_int
+    lib.quest_act8_load.argtypes = [vp, vp, i64, i64, vp, c_int, vp]
+    lib.quest_act8_load.restype = c_int
+    lib.quest_layer_norm_fwd.argtypes = [vp, c_int, i64, i64, vp, vp, c_int, ctypes.c_double, vp, vp, vp, vp, vp, vp]
+    lib.quest_layer_norm_fwd.restype = c_int
+    lib.quest_layer_norm_workspace_bytes.argtypes = [i64, i64]
+    lib.quest_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.quest_layer_norm_bwd.argtypes = [vp, c_int, i64, i64, vp, vp, vp, vp, vp, vp, c_int, vp, vp, vp, vp, vp]
+    lib.quest_layer_norm_bwd.restype = c_int
+    lib.quest_gated_fwd.argtypes = [vp, vp, i64, c_int, vp, vp, vp, vp, i64, c_int, i64, c_int, vp, c_int, vp, vp, vp,
+                                    vp, vp]
+    lib.quest_gated_fwd.restype = c_int
+    lib.quest_gated_bwd.argtypes = [vp, c_int, i64, i64, vp, vp, vp, vp, c_int, vp, vp]
+    lib.quest_gated_bwd.restype = c_int
     lib.quest_status_string.argtypes = [c_int]
     lib.quest_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -621,4 +653,229 @@ def trust_bwd(grad: torch.Tensor, mask: torch.Tensor, block: int, out=None, stre
         out.data_ptr(), _stream_handle(grad.device, stream),
     )
     _check("quest_trust_bwd", st)
+    return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(call: str, dev: torch.device, stream, *args) -> None:
+    """One device call of the library on `stream` (default: dev's current stream), with dev the current device."""
+    fn = getattr(load_library(), call)
+    if torch.cuda.current_device() == dev.index:
+        _check(call, fn(*args, _stream_handle(dev, stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call, fn(*args, _stream_handle(dev, stream)))
+
+
+def _matrix(name: str, t) -> None:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor (rows x cols)")
+    _dtype_code(t)
+
+
+def _exactly(name: str, t, dtype, shape) -> None:
+    """A caller's tensor of this type and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _act8_pair(name: str, pair, rows: int, cols: int):
+    """(codes, scale) of an 8-bit checkpoint of a rows x cols tensor."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+        raise TypeError(f"{name} must be the (codes, scale) pair of an 8-bit checkpoint")
+    codes, scale = pair
+    _exactly(f"{name} codes", codes, torch.int8, (rows, cols))
+    _exactly(f"{name} scale", scale, torch.uint8, (rows, -(-cols // 32)))
+    return codes, scale
+
+
+def _new_act8(rows: int, cols: int, device):
+    return (torch.empty((rows, cols), dtype=torch.int8, device=device),
+            torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=device))
+
+
+def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
+    """8-bit checkpoint of a 2-D activation (quest_act8_save); returns (codes, scale).
+
+    codes: int8 (rows, cols); scale: uint8 (rows, ceil(cols / 32)), the biased
+    power-of-two exponent of each block of 32 columns.  Allocated unless given.
+    """
+    _matrix("x", x)
+    rows, cols = x.shape
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=x.device)
+    _act8_pair("the checkpoint's", (codes, scale), rows, cols)
+    _on_device(x.device, x=x, codes=codes, scale=scale)
+    _launch("quest_act8_save", x.device, stream, x.data_ptr(), _dtype_code(x), rows, cols, codes.data_ptr(),
+            scale.data_ptr())
+    return codes, scale
+
+
+def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16, out=None,
+              stream=None) -> torch.Tensor:
+    """The values of an 8-bit checkpoint (quest_act8_load), exact in bfloat16 and float32."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be a 2-D tensor (rows x cols)")
+    rows, cols = codes.shape
+    _act8_pair("the checkpoint's", (codes, scale), rows, cols)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
+    _matrix("out", out)
+    _exactly("out", out, out.dtype, (rows, cols))
+    _on_device(codes.device, codes=codes, scale=scale, out=out)
+    _launch("quest_act8_load", codes.device, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(),
+            _dtype_code(out))
+    return out
+
+
+def _norm_params(cols: int, weight, bias):
+    """The tensors among weight and bias by name, and their common type's code."""
+    given = {k: t for k, t in (("weight", weight), ("bias", bias)) if t is not None}
+    code = QUEST_F32
+    for name, t in given.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        code = _dtype_code(t)
+        _exactly(name, t, t.dtype, (cols,))
+    if len(given) == 2 and weight.dtype != bias.dtype:
+        raise TypeError(f"weight and bias must share one type, got {weight.dtype} and {bias.dtype}")
+    return given, code
+
+
+def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, act8: bool = False, out=None,
+                   stream=None):
+    """Layer norm of each row of a 2-D tensor (quest_layer_norm_fwd).
+
+    weight, bias: (cols,) of one type, float32 or bfloat16, or None.
+    Returns (y, mean, rstd, act8): y of x's type, mean and rstd float32
+    (rows,), and with act8 the (codes, scale) of the normalised input's 8-bit
+    checkpoint for layer_norm_bwd (otherwise None).
+    """
+    _matrix("x", x)
+    rows, cols = x.shape
+    dev = x.device
+    given, param_code = _norm_params(cols, weight, bias)
+    if out is None:
+        out = torch.empty_like(x)
+    _exactly("out", out, x.dtype, (rows, cols))
+    _on_device(dev, x=x, out=out, **given)
+    mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+    rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    codes, scale = _new_act8(rows, cols, dev) if act8 else (None, None)
+    _launch("quest_layer_norm_fwd", dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ptr(weight), _ptr(bias),
+            param_code, float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(codes), _ptr(scale))
+    return out, mean, rstd, (codes, scale) if act8 else None
+
+
+def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None, mean=None, act8=None,
+                   input_grad: bool = True, weight_grad: bool | None = None, bias_grad: bool = False,
+                   param_dtype=None, stream=None):
+    """Backward pass of layer_norm_fwd (quest_layer_norm_bwd); returns (dx, dweight, dbias).
+
+    The forward's input comes as x and mean, or as its checkpoint act8 =
+    (codes, scale).  weight_grad defaults to whether a weight is given; what is
+    not asked for is None.  Parameter gradients have the weight's type, or
+    param_dtype (default float32) without one.
+    """
+    _matrix("dy", dy)
+    rows, cols = dy.shape
+    dev = dy.device
+    if weight_grad is None:
+        weight_grad = weight is not None
+    if not (input_grad or weight_grad or bias_grad):
+        raise ValueError("no gradient is asked for")
+    if (act8 is None) == (x is None) or (x is None) != (mean is None):
+        raise ValueError("give x and mean, or act8")
+    given, _ = _norm_params(cols, weight, None)
+    _exactly("rstd", rstd, torch.float32, (rows,))
+    codes = scale = None
+    if act8 is None:
+        _exactly("x", x, dy.dtype, (rows, cols))
+        _exactly("mean", mean, torch.float32, (rows,))
+        given.update(x=x, mean=mean)
+    else:
+        codes, scale = _act8_pair("act8", act8, rows, cols)
+        given.update(codes=codes, scale=scale)
+    param_dtype = weight.dtype if weight is not None else param_dtype or torch.float32
+    if param_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"parameter gradients are float32 or bfloat16, not {param_dtype}")
+    _on_device(dev, dy=dy, rstd=rstd, **given)
+    dx = torch.empty_like(dy) if input_grad else None
+    dweight = torch.empty((cols,), dtype=param_dtype, device=dev) if weight_grad else None
+    dbias = torch.empty((cols,), dtype=param_dtype, device=dev) if bias_grad else None
+    ws = None
+    if weight_grad or bias_grad:
+        need = int(load_library().quest_layer_norm_workspace_bytes(rows, cols))
+        ws = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+        if stream is not None and stream != torch.cuda.current_stream(dev):
+            ws.record_stream(stream)  # its memory is not handed out again before the call there has run
+    _launch("quest_layer_norm_bwd", dev, stream, dy.data_ptr(), _dtype_code(dy), rows, cols, _ptr(x), _ptr(mean),
+            _ptr(codes), _ptr(scale), rstd.data_ptr(), _ptr(weight),
+            QUEST_BF16 if param_dtype == torch.bfloat16 else QUEST_F32, _ptr(dx), _ptr(dweight), _ptr(dbias),
+            _ptr(ws))
+    return dx, dweight, dbias
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, not {act!r}")
+    return ACTIVATIONS[act]
+
+
+def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate: torch.Tensor,
+              gate_scale: torch.Tensor, up: torch.Tensor, up_scale: torch.Tensor, m: int, w_bits: int, k: int,
+              act: str = "silu", out_dtype=torch.bfloat16, act8: bool = False, out=None, stream=None):
+    """act(Q(x) Q(gate)^T) * (Q(x) Q(up)^T) of matrix-core operands (quest_gated_fwd).
+
+    x is the operand of n rows, gate and up those of m rows each, all of k
+    columns, with their clip scales, as for gemm.  Returns (h, gate8, up8): h
+    (n, m) of out_dtype and, with act8, the (codes, scale) checkpoints of both
+    products for gated_bwd (otherwise None).
+    """
+    n, m, k = int(n), int(m), int(k)
+    code = _act_code(act)
+    for name, t, rows in (("x", x, n), ("gate", gate, m), ("up", up, m)):
+        _buffer(name, t, torch.uint8, operand_bytes(rows, k))
+    for name, t, rows in (("x_scale", x_scale, n), ("gate_scale", gate_scale, m), ("up_scale", up_scale, m)):
+        _buffer(name, t, torch.float32, rows)
+    dev = x.device
+    if out is None:
+        out = torch.empty((n, m), dtype=out_dtype, device=dev)
+    _matrix("out", out)
+    _exactly("out", out, out.dtype, (n, m))
+    _on_device(dev, x=x, x_scale=x_scale, gate=gate, gate_scale=gate_scale, up=up, up_scale=up_scale, out=out)
+    gate8 = _new_act8(n, m, dev) if act8 else (None, None)
+    up8 = _new_act8(n, m, dev) if act8 else (None, None)
+    _launch("quest_gated_fwd", dev, stream, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
+            gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(), m, int(w_bits), k, code, out.data_ptr(),
+            _dtype_code(out), _ptr(gate8[0]), _ptr(gate8[1]), _ptr(up8[0]), _ptr(up8[1]))
+    return (out, gate8, up8) if act8 else (out, None, None)
+
+
+def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=None) -> torch.Tensor:
+    """Backward pass of gated_fwd from its checkpoints (quest_gated_bwd).
+
+    Returns (rows, 2 cols) of dh's type: the gradient reaching the gate product
+    in the first cols columns, the one reaching the up product in the others.
+    """
+    _matrix("dh", dh)
+    rows, cols = dh.shape
+    code = _act_code(act)
+    gc, gs = _act8_pair("gate8", gate8, rows, cols)
+    uc, us = _act8_pair("up8", up8, rows, cols)
+    if out is None:
+        out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dh.device)
+    _exactly("out", out, dh.dtype, (rows, 2 * cols))
+    _on_device(dh.device, dh=dh, gate_codes=gc, gate_scale=gs, up_codes=uc, up_scale=us, out=out)
+    _launch("quest_gated_bwd", dh.device, stream, dh.data_ptr(), _dtype_code(dh), rows, cols, gc.data_ptr(),
+            gs.data_ptr(), uc.data_ptr(), us.data_ptr(), code, out.data_ptr())
     return out

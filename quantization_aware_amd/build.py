@@ -27,12 +27,15 @@ SOURCES = [
     "quest_fwd_op.hip",
     "quest_gemm.hip",
     "quest_grids.hip",
+    "quest_act8.hip",
+    "quest_norm.hip",
+    "quest_gated.hip",
 ]
 # Sources built without the VGPR-only MFMA form, leaving the placement of the
-# matrix-core accumulators to the register allocator (the product kernel, whose
+# matrix-core accumulators to the register allocator (the product kernels, whose
 # 128 accumulator registers per wave share the 256-register budget of two
 # waves per SIMD: the VGPR-only form spilled there).
-AGPR_SOURCES = {"quest_gemm.hip"}
+AGPR_SOURCES = {"quest_gemm.hip", "quest_gated.hip"}
 ARCH = "gfx950"
 NOISE = "is not a recognized feature for this target"  # the host pass does not know the GPU feature below
 

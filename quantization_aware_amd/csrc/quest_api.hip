@@ -150,14 +150,42 @@ size_t dtype_size(quest_dtype d) { return d == QUEST_BF16 ? 2 : 4; }
 
 bool dtype_ok(quest_dtype d) { return d == QUEST_F32 || d == QUEST_BF16; }
 
+bool act_ok(quest_act a) { return a == QUEST_SILU || a == QUEST_GELU; }
+
+// A buffer of a call (NULL: not given) and whether the call writes it.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+
+// Every given buffer 16-byte aligned, and no written one overlapping another.
+quest_status check_spans(const Span* s, int count) {
+  for (int i = 0; i < count; ++i)
+    if (s[i].p && !aligned16(s[i].p)) return QUEST_EALIGN;
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < i; ++j)
+      if (s[i].p && s[j].p && (s[i].written || s[j].written) && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes))
+        return QUEST_EINVAL;
+  return QUEST_OK;
+}
+
 // rows * cols must stay below 2^36 so that the number of 32-element runs fits
 // in 31 bits.
 constexpr int64_t kMaxElements = int64_t(1) << 36;
+constexpr int64_t kMaxAct8Cols = int64_t(1) << 20;
 
 quest_status check_shape(int64_t rows, int64_t cols, int multiple_of) {
   if (rows < 0 || cols <= 0 || cols % multiple_of != 0) return QUEST_EINVAL;
   if (cols > QUEST_MAX_COLS) return QUEST_EUNSUPPORTED;
   if (rows > kMaxElements / cols) return QUEST_EUNSUPPORTED;
+  return QUEST_OK;
+}
+
+// Checkpoints of any width that quest_gated_fwd can write.
+quest_status check_act8_shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0) return QUEST_EINVAL;
+  if (cols > kMaxAct8Cols || rows > kMaxElements / cols) return QUEST_EUNSUPPORTED;
   return QUEST_OK;
 }
 
@@ -536,6 +564,210 @@ quest_status quest_trust_bwd(const void* grad, quest_dtype g_dtype, const uint8_
   std::call_once(g_env_once, read_env);
   return from_hip(quest::launch_trust_bwd(grad, g_dtype == QUEST_BF16, mask, rows, cols, lb, grad_out,
                                           g_allow_mfma_bwd, static_cast<hipStream_t>(stream)));
+}
+
+size_t quest_act8_scale_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0 || rows > kMaxElements / cols) return 0;
+  return static_cast<size_t>(rows) * static_cast<size_t>((cols + 31) / 32);
+}
+
+quest_status quest_act8_save(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, int8_t* codes,
+                             uint8_t* scale, void* stream) {
+  if (!dtype_ok(x_dtype)) return QUEST_EINVAL;
+  const quest_status sh = check_act8_shape(rows, cols);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!x || !codes || !scale) return QUEST_EINVAL;
+  const size_t n = static_cast<size_t>(rows * cols);
+  const Span spans[] = {{x, n * dtype_size(x_dtype), false}, {codes, n, true},
+                        {scale, quest_act8_scale_bytes(rows, cols), true}};
+  const quest_status st = check_spans(spans, 3);
+  if (st != QUEST_OK) return st;
+  return from_hip(quest::launch_act8_save(x, x_dtype == QUEST_BF16, rows, static_cast<int>(cols), codes, scale,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+quest_status quest_act8_load(const int8_t* codes, const uint8_t* scale, int64_t rows, int64_t cols, void* out,
+                             quest_dtype out_dtype, void* stream) {
+  if (!dtype_ok(out_dtype)) return QUEST_EINVAL;
+  const quest_status sh = check_act8_shape(rows, cols);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!codes || !scale || !out) return QUEST_EINVAL;
+  const size_t n = static_cast<size_t>(rows * cols);
+  const Span spans[] = {{codes, n, false}, {scale, quest_act8_scale_bytes(rows, cols), false},
+                        {out, n * dtype_size(out_dtype), true}};
+  const quest_status st = check_spans(spans, 3);
+  if (st != QUEST_OK) return st;
+  return from_hip(quest::launch_act8_load(codes, scale, rows, static_cast<int>(cols), out, out_dtype == QUEST_BF16,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+quest_status quest_layer_norm_fwd(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, const void* weight,
+                                  const void* bias, quest_dtype param_dtype, double eps, void* y, float* mean,
+                                  float* rstd, int8_t* codes, uint8_t* scale, void* stream) {
+  if (!dtype_ok(x_dtype) || ((weight || bias) && !dtype_ok(param_dtype))) return QUEST_EINVAL;
+  // eps is used in fp32, where it has to be a positive finite number
+  if (!(static_cast<float>(eps) > 0.0f) || !std::isfinite(static_cast<float>(eps))) return QUEST_EINVAL;
+  const quest_status sh = check_shape(rows, cols, 1);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!x || !y || (codes == nullptr) != (scale == nullptr)) return QUEST_EINVAL;
+  const size_t n = static_cast<size_t>(rows * cols), np = static_cast<size_t>(cols) * dtype_size(param_dtype);
+  const size_t nx = n * dtype_size(x_dtype), nr = static_cast<size_t>(rows) * sizeof(float);
+  const Span spans[] = {{x, nx, false},   {weight, np, false}, {bias, np, false}, {y, nx, true},
+                        {mean, nr, true}, {rstd, nr, true},    {codes, n, true},
+                        {scale, quest_act8_scale_bytes(rows, cols), true}};
+  const quest_status st = check_spans(spans, 8);
+  if (st != QUEST_OK) return st;
+  quest::NormFwdLaunch a;
+  a.x = x;
+  a.rows = rows;
+  a.cols = static_cast<int>(cols);
+  a.weight = weight;
+  a.bias = bias;
+  a.param_bf16 = param_dtype == QUEST_BF16;
+  a.eps = static_cast<float>(eps);
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scale = scale;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_norm_fwd(a, x_dtype == QUEST_BF16));
+}
+
+size_t quest_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0 || cols > QUEST_MAX_COLS || rows > kMaxElements / cols) return 0;
+  return static_cast<size_t>(quest::norm_bwd_groups(rows, cols)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+}
+
+quest_status quest_layer_norm_bwd(const void* dy, quest_dtype dtype, int64_t rows, int64_t cols, const void* x,
+                                  const float* mean, const int8_t* codes, const uint8_t* scale, const float* rstd,
+                                  const void* weight, quest_dtype param_dtype, void* dx, void* dweight, void* dbias,
+                                  void* workspace, void* stream) {
+  const bool params = dweight || dbias;
+  if (!dtype_ok(dtype) || ((weight || params) && !dtype_ok(param_dtype))) return QUEST_EINVAL;
+  const quest_status sh = check_shape(rows, cols, 1);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0 && !params) return QUEST_OK;
+  const size_t np = static_cast<size_t>(cols) * dtype_size(param_dtype);
+  const size_t n = static_cast<size_t>(rows * cols), nx = n * dtype_size(dtype);
+  const size_t nr = static_cast<size_t>(rows) * sizeof(float);
+  if (rows > 0) {
+    if (!dy || !rstd || (!dx && !params) || (params && !workspace)) return QUEST_EINVAL;
+    // the input is x with its mean, or the checkpoint
+    if (codes ? (!scale || x || mean) : (scale || !x || !mean)) return QUEST_EINVAL;
+  }
+  const Span spans[] = {{dy, nx, false},
+                        {x, nx, false},
+                        {mean, nr, false},
+                        {codes, n, false},
+                        {scale, quest_act8_scale_bytes(rows, cols), false},
+                        {rstd, nr, false},
+                        {weight, np, false},
+                        {dx, nx, true},
+                        {dweight, np, true},
+                        {dbias, np, true},
+                        {params ? workspace : nullptr, quest_layer_norm_workspace_bytes(rows, cols), true}};
+  const quest_status st = check_spans(spans, 11);
+  if (st != QUEST_OK) return st;
+  quest::NormBwdLaunch a;
+  a.dy = dy;
+  a.rows = rows;
+  a.cols = static_cast<int>(cols);
+  a.x = x;
+  a.mean = mean;
+  a.codes = codes;
+  a.scale = scale;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.param_bf16 = param_dtype == QUEST_BF16;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.workspace = params ? static_cast<float*>(workspace) : nullptr;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_norm_bwd(a, dtype == QUEST_BF16));
+}
+
+quest_status quest_gated_fwd(const uint8_t* x, const float* x_scale, int64_t n, int x_bits, const uint8_t* gate,
+                             const float* gate_scale, const uint8_t* up, const float* up_scale, int64_t m, int w_bits,
+                             int64_t k, quest_act act, void* out, quest_dtype out_dtype, int8_t* gate_codes,
+                             uint8_t* gate_exp, int8_t* up_codes, uint8_t* up_exp, void* stream) {
+  if (x_bits < 1 || x_bits > 4 || w_bits < 1 || w_bits > 4) return QUEST_EUNSUPPORTED;
+  if (!dtype_ok(out_dtype) || !act_ok(act) || n < 0 || m < 0 || k <= 0) return QUEST_EINVAL;
+  if (k % 128 != 0 || k > kGemmMaxK || m > kGemmMaxN || n > kGemmMaxM) return QUEST_EUNSUPPORTED;
+  // 512 work-items per tile: the launch's work-item count must fit 32 bits.
+  if (((n + 255) / 256) * ((m + 127) / 128) > kGemmMaxTiles) return QUEST_EUNSUPPORTED;
+  if (n == 0 || m == 0) return QUEST_OK;
+  if (!x || !x_scale || !gate || !gate_scale || !up || !up_scale || !out) return QUEST_EINVAL;
+  const bool keep = gate_codes != nullptr;
+  if ((gate_exp != nullptr) != keep || (up_codes != nullptr) != keep || (up_exp != nullptr) != keep)
+    return QUEST_EINVAL;
+  const size_t e = static_cast<size_t>(n) * static_cast<size_t>(m);
+  const size_t ne = static_cast<size_t>(n) * static_cast<size_t>((m + 31) / 32);
+  const size_t nw = quest_operand_bytes(m, k), nm = static_cast<size_t>(m) * sizeof(float);
+  const Span spans[] = {{x, quest_operand_bytes(n, k), false},
+                        {x_scale, static_cast<size_t>(n) * sizeof(float), false},
+                        {gate, nw, false},
+                        {gate_scale, nm, false},
+                        {up, nw, false},
+                        {up_scale, nm, false},
+                        {out, e * dtype_size(out_dtype), true},
+                        {gate_codes, e, true},
+                        {gate_exp, ne, true},
+                        {up_codes, e, true},
+                        {up_exp, ne, true}};
+  const quest_status st = check_spans(spans, 11);
+  if (st != QUEST_OK) return st;
+  quest::GatedLaunch g;
+  g.x = x;
+  g.sx = x_scale;
+  g.n = static_cast<int>(n);
+  g.gate = gate;
+  g.sg = gate_scale;
+  g.up = up;
+  g.su = up_scale;
+  g.m = static_cast<int>(m);
+  g.k = static_cast<int>(k);
+  g.kx = static_cast<float>(2.0 / double((1 << x_bits) - 1));
+  g.kw = static_cast<float>(2.0 / double((1 << w_bits) - 1));
+  g.act = static_cast<int>(act);
+  g.out = out;
+  g.gate_codes = gate_codes;
+  g.gate_scale = gate_exp;
+  g.up_codes = up_codes;
+  g.up_scale = up_exp;
+  g.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_gated_fwd(g, out_dtype == QUEST_BF16));
+}
+
+quest_status quest_gated_bwd(const void* dh, quest_dtype dtype, int64_t rows, int64_t cols, const int8_t* gate_codes,
+                             const uint8_t* gate_exp, const int8_t* up_codes, const uint8_t* up_exp, quest_act act,
+                             void* out, void* stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || rows < 0 || cols < 0) return QUEST_EINVAL;
+  if (cols > kGemmMaxN || rows > kGemmMaxM || (cols > 0 && rows > kMaxElements / cols)) return QUEST_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return QUEST_OK;
+  if (!dh || !gate_codes || !gate_exp || !up_codes || !up_exp || !out) return QUEST_EINVAL;
+  const size_t e = static_cast<size_t>(rows * cols);
+  const size_t ne = quest_act8_scale_bytes(rows, cols);
+  const Span spans[] = {{dh, e * dtype_size(dtype), false}, {gate_codes, e, false}, {gate_exp, ne, false},
+                        {up_codes, e, false},               {up_exp, ne, false},    {out, 2 * e * dtype_size(dtype), true}};
+  const quest_status st = check_spans(spans, 6);
+  if (st != QUEST_OK) return st;
+  quest::GatedBwdLaunch a;
+  a.dh = dh;
+  a.rows = rows;
+  a.cols = static_cast<int>(cols);
+  a.gate_codes = gate_codes;
+  a.gate_scale = gate_exp;
+  a.up_codes = up_codes;
+  a.up_scale = up_exp;
+  a.act = static_cast<int>(act);
+  a.out = out;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_gated_bwd(a, dtype == QUEST_BF16));
 }
 
 }  // extern "C"

@@ -1,0 +1,388 @@
+// The gated feed-forward product of quantised operands and its backward pass.
+//
+//   g = Q(x) Q(gate)^T,  u = Q(x) Q(up)^T,  h = act(g) * u,
+// with the operands of quest_gemm: FP6 E2M3 levels, tiled in blocks of 32 rows
+// x 128 columns (include/quest.h).  Both products, the activation and the
+// product are one kernel: g and u never leave the registers in more than the
+// 8 bits of their checkpoints (quest_act8.h), which the training form writes.
+// The levels' products are quarter-integers whose sums stay below 2^22, so the
+// fp32 accumulation is exact in any order, and
+//   g[i][j] = acc[i][j] * ((sx[i] kx) * (sg[j] kw))
+// has three roundings and then the activation's.
+//
+// Kernel: a workgroup of 8 waves computes 256 rows x 128 columns of h.  The
+// two weight operands' 4 + 4 blocks of 32 columns stand side by side in a
+// stage of LDS, so that a wave of 64 rows x 64 columns holds its gate and up
+// accumulators (2 x 2 blocks of 32 columns by 2 blocks of 32 rows) in the same
+// lanes and registers: lane l has row l % 32 and 4 consecutive columns per
+// register quad of both.  Stages stream into LDS three deep, as in quest_gemm.
+#include <type_traits>
+
+#include "quest_act8.h"
+#include "quest_launch.h"
+#include "quest_mma.h"
+
+namespace quest {
+namespace {
+
+constexpr int kRowsTile = 256, kColsTile = 128;  // workgroup tile of h
+constexpr int kXStage = 8 * kBlock;              // x's 256 rows of a stage
+constexpr int kStage = 2 * kXStage;              // and 4 + 4 blocks of gate and up
+
+// act(g) and act'(g).  kFast: the hardware's reciprocal and exp2 (about 2^-22
+// relative), for values that are rounded to bf16 next; fp32 results take the
+// full-precision functions.
+template <bool kFast>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (kFast) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+  return 1.0f / (1.0f + expf(-g));
+}
+template <bool kFast>
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == 0) return g * sigmoid<kFast>(g);
+  return 0.5f * g * erfcf(g * -0.707106781f);
+}
+template <bool kFast>
+__device__ __forceinline__ void act_both(float g, int act, float& value, float& slope) {
+  if (act == 0) {
+    const float s = sigmoid<kFast>(g);
+    value = g * s;
+    slope = fmaf(value, 1.0f - s, s);
+  } else {
+    const float phi = 0.5f * erfcf(g * -0.707106781f);
+    value = g * phi;
+    slope = fmaf(g * 0.398942280f, expf(-0.5f * g * g), phi);
+  }
+}
+
+template <typename Out, bool kVec, bool kAct8>
+__global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a) {
+  constexpr int kOut = static_cast<int>(sizeof(Out));
+  constexpr int kPer = 16 / kOut;             // outputs per 16-byte chunk
+  constexpr int kLanesPerRow = 64 / kPer;     // a wave's 64 columns
+  constexpr int kPitch = 64 * kOut + 16;      // slab row pitch in bytes
+  constexpr int kPitch8 = 128 + 16;           // codes: 64 of gate, 64 of up
+  static_assert(8 * 32 * kPitch <= 2 * kStage && kPitch8 <= kPitch, "slabs fit the second and third stage buffers");
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage + (256 + 2 * 128) * 4];
+  auto stage_mem = [&](auto bi) -> uint8_t* { return lds + decltype(bi)::value * kStage; };
+  float* const fac = reinterpret_cast<float*>(lds + 3 * kStage);  // [256] x, [128] gate, [128] up clip scales
+
+  const int n = a.n, m = a.m, k = a.k;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int lane = tid & 63;
+  const int stages = k >> 7;
+  const uint32_t rb_bytes = static_cast<uint32_t>(stages) * kBlock;  // one 32-row block, all of k
+  const int tiles_m = (n + kRowsTile - 1) / kRowsTile, tiles_n = (m + kColsTile - 1) / kColsTile;
+  // Workgroups are dealt to the 8 XCDs round-robin; each XCD takes a
+  // contiguous range of tiles, whose operand blocks then share its L2.
+  int pid = blockIdx.x, tm, tn;
+  const int full = static_cast<int>(gridDim.x) & ~7;
+  if (pid < full) pid = (pid & 7) * (full >> 3) + (pid >> 3);
+  tile_at(pid, tiles_m, tiles_n, tm, tn);
+  const int row0 = tm * kRowsTile, col0 = tn * kColsTile;
+
+  const int rb_x = (n + 31) >> 5, rb_w = (m + 31) >> 5;
+  const i32x4 rx = raw_rsrc(a.x + static_cast<size_t>(tm) * 8 * rb_bytes, min(rb_x - tm * 8, 8) * rb_bytes);
+  const uint32_t w_bytes = min(rb_w - tn * 4, 4) * rb_bytes;
+  const i32x4 rg = raw_rsrc(a.gate + static_cast<size_t>(tn) * 4 * rb_bytes, w_bytes);
+  const i32x4 ru = raw_rsrc(a.up + static_cast<size_t>(tn) * 4 * rb_bytes, w_bytes);
+
+  // The clip scales: wave w < 4 rows 64 w ..., waves 4 and 5 gate's columns, 6 and 7 up's.
+  {
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(fac)) + 256 * wave;
+    const float* src = wave < 4 ? a.sx + row0 + 64 * wave : (wave < 6 ? a.sg : a.su) + col0 + 64 * (wave & 1);
+    const int left = wave < 4 ? n - row0 - 64 * wave : m - col0 - 64 * (wave & 1);
+    dma4(base, lane * 4, raw_rsrc(src, __builtin_amdgcn_readfirstlane(max(min(left, 64), 0)) * 4));
+  }
+
+  // Stage st into LDS: 24 wave instructions for x and 24 for the weights,
+  // wave w issuing w + 8 u, u < 3, of each.
+  constexpr int kLoads = 6;
+  auto fetch_stage = [&](int st, auto bi) {
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage_mem(bi)));
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const int t = wave + 8 * u, blk = t / 3, part = t % 3;
+      const int off = st * kBlock + part * 1024 + lane * 16;
+      const uint32_t la = base + blk * kBlock + part * 1024;
+      dma16(__builtin_amdgcn_readfirstlane(la), blk * static_cast<int>(rb_bytes) + off, rx);
+      dma16(__builtin_amdgcn_readfirstlane(la + kXStage), (blk & 3) * static_cast<int>(rb_bytes) + off,
+            blk < 4 ? rg : ru);
+    }
+  };
+  // Fragment (block rbk of x (op 0) or of the weights (op 1), k-half ks): this lane's 24 bytes.
+  auto frag = [&](auto bi, int op, int rbk, int ks) -> v8i {
+    const u32x2* s =
+        reinterpret_cast<const u32x2*>(stage_mem(bi) + op * kXStage + rbk * kBlock + ks * kFrag + lane * 24);
+    const u32x2 x0 = s[0], x1 = s[1], x2 = s[2];
+    return v8i{static_cast<int>(x0[0]), static_cast<int>(x0[1]), static_cast<int>(x1[0]),
+               static_cast<int>(x1[1]), static_cast<int>(x2[0]), static_cast<int>(x2[1]), 0, 0};
+  };
+  // Weight block j of a wave: gate 2 wn, 2 wn + 1, then up's.
+  auto wblk = [&](int j) { return (j & 1) + 2 * wn + 4 * (j >> 1); };
+
+  fetch_stage(0, I0{});
+  fetch_stage(stages > 1 ? 1 : 0, I1{});
+  v16f acc[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[j][i] = v16f{};
+  wait_vmcnt<kLoads>();
+  lds_barrier();
+  v8i f0x[2], f0w[4], f1x[2], f1w[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f0x[i] = frag(I0{}, 0, wm * 2 + i, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f0w[j] = frag(I0{}, 1, wblk(j), 0);
+  // One stage: bi holds stage s, bn stage s + 1, b2 receives stage s + 2 (it
+  // last held stage s - 1, whose reads every wave finished before the previous
+  // barrier).  Stages past the last are the last one again, so that every wait
+  // counts the same loads.
+  auto step = [&](int s, auto bi, auto bn, auto b2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f1x[i] = frag(bi, 0, wm * 2 + i, 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f1w[j] = frag(bi, 1, wblk(j), 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0w[j], f0x[i], acc[j][i], 2, 2, 0, 127, 0, 127);
+    fetch_stage(s + 2 < stages ? s + 2 : stages - 1, b2);
+    wait_vmcnt<kLoads>();
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f0x[i] = frag(bn, 0, wm * 2 + i, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f0w[j] = frag(bn, 1, wblk(j), 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1w[j], f1x[i], acc[j][i], 2, 2, 0, 127, 0, 127);
+  };
+  int s = 0;
+  for (; s + 3 <= stages; s += 3) {
+    step(s, I0{}, I1{}, I2{});
+    step(s + 1, I1{}, I2{}, I0{});
+    step(s + 2, I2{}, I0{}, I1{});
+  }
+  if (s < stages) step(s++, I0{}, I1{}, I2{});
+  if (s < stages) step(s++, I1{}, I2{}, I0{});
+  wait_vmcnt<0>();  // no load into LDS in flight before it is reused
+  lds_barrier();
+
+  // Epilogue: each wave goes through its two blocks of 32 rows, in a slab of
+  // LDS of its own.
+  uint8_t* slab = lds + kStage + wave * 32 * kPitch;
+  const int rows_left = min(n - row0, kRowsTile);
+  const auto rout = make_rsrc(static_cast<Out*>(a.out) + static_cast<size_t>(row0) * m,
+                              static_cast<uint32_t>(rows_left) * static_cast<uint32_t>(m) * kOut);
+  const int r32 = lane & 31, h = lane >> 5;
+  const int wcol = col0 + wn * 64;  // the wave's first column
+  auto slab_fence = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float fx = fac[wm * 64 + 32 * i + r32] * a.kx;
+    uint32_t code[2][2][4];  // [gate, up][block][quad]
+    int ex[2][2];
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      uint32_t mg = 0, mu = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int cl = 32 * jj + 8 * q + 4 * h;  // column within the wave's 64
+        const float4 sg = *reinterpret_cast<const float4*>(&fac[256 + wn * 64 + cl]);
+        const float4 su = *reinterpret_cast<const float4*>(&fac[384 + wn * 64 + cl]);
+        const float kg[4] = {sg.x, sg.y, sg.z, sg.w}, ku[4] = {su.x, su.y, su.z, su.w};
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float gv = acc[jj][i][4 * q + e] * (fx * (kg[e] * a.kw));
+          const float uv = acc[2 + jj][i][4 * q + e] * (fx * (ku[e] * a.kw));
+          y[e] = act_value<kOut == 2>(gv, a.act) * uv;
+          if constexpr (kAct8) {
+            acc[jj][i][4 * q + e] = gv;
+            acc[2 + jj][i][4 * q + e] = uv;
+            if (wcol + cl + e < m) {
+              mg = max(mg, act8_mag(gv));
+              mu = max(mu, act8_mag(uv));
+            }
+          }
+        }
+        uint8_t* d = slab + r32 * kPitch + cl * kOut;
+        if constexpr (kOut == 4) {
+          *reinterpret_cast<u32x4*>(d) =
+              u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
+        } else {
+          *reinterpret_cast<u32x2*>(d) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        }
+      }
+      if constexpr (kAct8) {
+        // the block's other 16 columns are in lane ^ 32
+        mg = max(mg, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mg), 32, 64)));
+        mu = max(mu, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mu), 32, 64)));
+        ex[0][jj] = static_cast<int>(mg >> 23);
+        ex[1][jj] = static_cast<int>(mu >> 23);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            int c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = act8_encode(acc[2 * p + jj][i][4 * q + e], ex[p][jj]);
+            code[p][jj][q] = act8_pack(c[0], c[1], c[2], c[3]);
+          }
+      }
+    }
+    slab_fence();
+#pragma unroll
+    for (int t = 0; t < 32 * kLanesPerRow / 64; ++t) {
+      const int sr = t * (64 / kLanesPerRow) + lane / kLanesPerRow, sc = (lane % kLanesPerRow) * kPer;
+      const int row = wm * 64 + 32 * i + sr, col = wcol + sc;
+      const uint8_t* src = slab + sr * kPitch + sc * kOut;
+      if constexpr (kVec) {
+        const int off = col < m ? (row * m + col) * kOut : kNowhereOff;
+        __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(src), rout, off, 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const int off = col + e < m ? (row * m + col + e) * kOut : kNowhereOff;
+          if constexpr (kOut == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t*>(src + 4 * e), rout, off, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t*>(src + 2 * e), rout, off, 0, 0);
+        }
+      }
+    }
+    slab_fence();
+    if constexpr (kAct8) {
+      const int blocks = (m + 31) >> 5;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint32_t*>(slab + r32 * kPitch8 + 64 * p + 32 * jj + 8 * q + 4 * h) = code[p][jj][q];
+      slab_fence();
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const auto rc = make_rsrc((p ? a.up_codes : a.gate_codes) + static_cast<size_t>(row0) * m,
+                                  static_cast<uint32_t>(rows_left) * static_cast<uint32_t>(m));
+        const auto re = make_rsrc((p ? a.up_scale : a.gate_scale) + static_cast<size_t>(row0) * blocks,
+                                  static_cast<uint32_t>(rows_left) * static_cast<uint32_t>(blocks));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int sr = t * 16 + lane / 4, sc = (lane % 4) * 16;
+          const int row = wm * 64 + 32 * i + sr, col = wcol + sc;
+          const uint8_t* src = slab + sr * kPitch8 + 64 * p + sc;
+          if constexpr (kVec) {
+            const int off = col < m ? row * m + col : kNowhereOff;
+            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(src), rc, off, 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              __builtin_amdgcn_raw_buffer_store_b8(src[e], rc, col + e < m ? row * m + col + e : kNowhereOff, 0, 0);
+          }
+        }
+        // the exponents of block h of the wave's two
+        const int blk = (wcol >> 5) + h;
+        const int e = h ? ex[p][1] : ex[p][0];
+        __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), re,
+                                             blk < blocks ? (wm * 64 + 32 * i + r32) * blocks + blk : kNowhereOff, 0,
+                                             0);
+      }
+      slab_fence();
+    }
+  }
+}
+
+// Backward: a row of the checkpoints per workgroup step, 8 columns a thread
+// (kVec, cols a multiple of 8) or one.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaunch a) {
+  const int cols = a.cols, blocks = (cols + kAct8Block - 1) / kAct8Block;
+  constexpr int kPer = kVec ? 8 : 1;
+  constexpr bool kFast = sizeof(T) == 2;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* dh = static_cast<const T*>(a.dh) + row * cols;
+    const int8_t* gc = a.gate_codes + row * cols;
+    const int8_t* uc = a.up_codes + row * cols;
+    const uint8_t* gs = a.gate_scale + row * blocks;
+    const uint8_t* us = a.up_scale + row * blocks;
+    T* dg = static_cast<T*>(a.out) + row * 2 * cols;
+    T* du = dg + cols;
+    for (int c = threadIdx.x * kPer; c < cols; c += 256 * kPer) {
+      const int eg = gs[c >> 5], eu = us[c >> 5];
+      if constexpr (kVec) {
+        float d[8], og[8], ou[8];
+        load8(dh + c, d);
+        const uint2 wg = *reinterpret_cast<const uint2*>(gc + c), wu = *reinterpret_cast<const uint2*>(uc + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = act8_decode(act8_byte(i < 4 ? wg.x : wg.y, i & 3), eg);
+          const float u = act8_decode(act8_byte(i < 4 ? wu.x : wu.y, i & 3), eu);
+          float value, slope;
+          act_both<kFast>(g, a.act, value, slope);
+          og[i] = d[i] * u * slope;
+          ou[i] = d[i] * value;
+        }
+        store8(dg + c, og);
+        store8(du + c, ou);
+      } else {
+        const float d = to_f32(dh[c]);
+        const float g = act8_decode(gc[c], eg), u = act8_decode(uc[c], eu);
+        float value, slope;
+        act_both<kFast>(g, a.act, value, slope);
+        dg[c] = from_f32<T>(d * u * slope);
+        du[c] = from_f32<T>(d * value);
+      }
+    }
+  }
+}
+
+template <typename Out, bool kVec>
+hipError_t launch(const GatedLaunch& g) {
+  const int tiles = ((g.n + kRowsTile - 1) / kRowsTile) * ((g.m + kColsTile - 1) / kColsTile);
+  if (g.gate_codes)
+    hipLaunchKernelGGL((quest_gated_kernel<Out, kVec, true>), dim3(tiles), dim3(512), 0, g.stream, g);
+  else
+    hipLaunchKernelGGL((quest_gated_kernel<Out, kVec, false>), dim3(tiles), dim3(512), 0, g.stream, g);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_bwd(const GatedBwdLaunch& a) {
+  const dim3 grid(static_cast<uint32_t>(a.rows < (1 << 20) ? a.rows : (1 << 20)));
+  if (a.cols % 8 == 0)
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, true>), grid, dim3(256), 0, a.stream, a);
+  else
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, false>), grid, dim3(256), 0, a.stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated_fwd(const GatedLaunch& g, bool out_bf16) {
+  // Rows whose chunks of 16 codes and of 16 bytes of output start on 16 bytes.
+  const bool vec = g.m % 16 == 0;
+  if (out_bf16) return vec ? launch<uint16_t, true>(g) : launch<uint16_t, false>(g);
+  return vec ? launch<float, true>(g) : launch<float, false>(g);
+}
+
+hipError_t launch_gated_bwd(const GatedBwdLaunch& a, bool bf16) {
+  return bf16 ? launch_bwd<uint16_t>(a) : launch_bwd<float>(a);
+}
+
+}  // namespace quest

@@ -121,4 +121,92 @@ hipError_t launch_dequantize_fp4(const uint8_t* codes, const float* scale, int64
 hipError_t launch_dequantize_sparse24(const uint8_t* codes, const uint8_t* index, const float* scale, int64_t rows,
                                       int64_t cols, int bits, void* out, int out_is_bf16, hipStream_t stream);
 
+// Activation checkpoints in 8 bits.  All sizes already validated.
+hipError_t launch_act8_save(const void* x, bool x_is_bf16, int64_t rows, int cols, int8_t* codes, uint8_t* scale,
+                            hipStream_t stream);
+hipError_t launch_act8_load(const int8_t* codes, const uint8_t* scale, int64_t rows, int cols, void* out,
+                            bool out_is_bf16, hipStream_t stream);
+
+// Layer norm's forward, already validated: weight, bias, mean, rstd and the
+// pair codes / scale (the 8-bit checkpoint of the normalised input) may be null.
+struct NormFwdLaunch {
+  const void* x;
+  int64_t rows;
+  int cols;
+  const void* weight;
+  const void* bias;
+  bool param_bf16;
+  float eps;
+  void* y;
+  float* mean;
+  float* rstd;
+  int8_t* codes;
+  uint8_t* scale;
+  hipStream_t stream;
+};
+hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16);
+
+// Its backward: x and mean, or codes and scale; dx, dweight and dbias may be
+// null, workspace (2 * norm_bwd_groups * cols floats) is null if both
+// dweight and dbias are.
+struct NormBwdLaunch {
+  const void* dy;
+  int64_t rows;
+  int cols;
+  const void* x;
+  const float* mean;
+  const int8_t* codes;
+  const uint8_t* scale;
+  const float* rstd;
+  const void* weight;
+  bool param_bf16;
+  void* dx;
+  void* dweight;
+  void* dbias;
+  float* workspace;
+  hipStream_t stream;
+};
+int norm_bwd_groups(int64_t rows, int64_t cols);  // workgroups, each with its own column sums
+hipError_t launch_norm_bwd(const NormBwdLaunch& a, bool bf16);
+
+// The gated product of quantised operands, already validated:
+// out (n x m) = act(x gate^T) * (x up^T); the 8-bit checkpoints of both
+// products (codes n x m, scale n x ceil(m / 32)) are written unless null.
+struct GatedLaunch {
+  const uint8_t* x;  // tiled E2M3 operands
+  const float* sx;
+  int n;
+  const uint8_t* gate;
+  const float* sg;
+  const uint8_t* up;
+  const float* su;
+  int m;
+  int k;     // a multiple of 128
+  float kx;  // 2 / (L_x - 1)
+  float kw;
+  int act;   // 0 silu, 1 gelu
+  void* out;
+  int8_t* gate_codes;
+  uint8_t* gate_scale;
+  int8_t* up_codes;
+  uint8_t* up_scale;
+  hipStream_t stream;
+};
+hipError_t launch_gated_fwd(const GatedLaunch& g, bool out_bf16);
+
+// Its backward from the checkpoints: out (rows x 2 cols) = [dh u act'(g) | dh act(g)].
+struct GatedBwdLaunch {
+  const void* dh;
+  int64_t rows;
+  int cols;
+  const int8_t* gate_codes;
+  const uint8_t* gate_scale;
+  const int8_t* up_codes;
+  const uint8_t* up_scale;
+  int act;
+  void* out;
+  hipStream_t stream;
+};
+hipError_t launch_gated_bwd(const GatedBwdLaunch& a, bool bf16);
+
 }  // namespace quest

@@ -1,0 +1,540 @@
+// Layer norm, forward and backward, and the form whose backward pass reads the
+// normalised input from its 8-bit checkpoint (quest_act8.h).
+//
+// Forward, per row of C entries (all in fp32):
+//   mean = sum x / C,  var = sum (x - mean)^2 / C,  rstd = 1 / sqrt(var + eps),
+//   xhat = (x - mean) rstd,  y = xhat w + b.
+// Backward, with a = dy w:
+//   dx = rstd (a - sum a / C - xhat sum(a xhat) / C),
+//   dw = sum_rows dy xhat,  db = sum_rows dy.
+//
+// One read of every input: a row's entries stay in the registers of the
+// threads that share it (64 for up to 2048 entries, so that its sums need no
+// barrier; a workgroup for wider rows).  The first sum gives the mean within
+// its rounding; the second pass over the registers sums x - near and its
+// square, which gives the rest of the mean and the variance about it, so a
+// large common offset costs no digits.
+// The parameter gradients: every workgroup of the backward kernel walks rows,
+// keeps its columns' sums in registers and writes them once; a second kernel
+// adds the workgroups' sums in a fixed order.  No atomics: the result depends
+// on the sizes alone.
+#include "quest_act8.h"
+
+#include "quest_launch.h"
+
+namespace quest {
+namespace {
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRowMask, 0xF, false));
+}
+// Sum over the 64 lanes, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_or_zero<0xB1, 0xF>(v);   // lane ^ 1
+  v += dpp_or_zero<0x4E, 0xF>(v);   // lane ^ 2
+  v += dpp_or_zero<0x141, 0xF>(v);  // the other quad of 8
+  v += dpp_or_zero<0x140, 0xF>(v);  // the other 8 of 16
+  v += dpp_or_zero<0x142, 0xA>(v);  // rows 1 and 3 add the row before
+  v += dpp_or_zero<0x143, 0xC>(v);  // rows 2 and 3 add row 1
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums of two values over the TPR threads of a row; `part` holds 2 * TPR / 64
+// floats and is free again after the next call's first barrier.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* part) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (TPR > 64) {
+    constexpr int kWaves = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+      part[2 * wave] = a;
+      part[2 * wave + 1] = b;
+    }
+    __syncthreads();
+    a = 0.0f;
+    b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      a += part[2 * w];
+      b += part[2 * w + 1];
+    }
+  }
+}
+
+// The columns of thread t of a row's TPR threads: kVec, groups of 8
+// neighbours 8 (t + TPR j); otherwise single columns t + TPR (8 j + i).
+template <int TPR, bool kVec>
+__device__ __forceinline__ int column(int t, int j, int i) {
+  return kVec ? 8 * (t + TPR * j) + i : t + TPR * (8 * j + i);
+}
+
+// A row (or a parameter vector) as a buffer resource: accesses past its end
+// read zero and write nothing, so no load or store stands behind a branch.  Its
+// base is rounded down to 4 bytes, `skip` is what that leaves in front.
+struct Row {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int skip;
+};
+__device__ __forceinline__ Row row_at(const void* p, int64_t first, int bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(first);
+  const int skip = static_cast<int>(at & 3);
+  return {__builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at - skip), static_cast<short>(0), bytes + skip,
+                                            0x00020000),
+          skip};
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32x4 load16(const Row& r, int off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, off, 0, 0);
+}
+
+// 8 entries of a row of T from index j of thread t; zeros past its end.
+template <typename T, int TPR, bool kVec>
+__device__ __forceinline__ void fetch(const Row& r, int t, int j, float (&v)[8]) {
+  if constexpr (kVec && sizeof(T) == 2) {
+    const u32x4 w = load16(r, column<TPR, true>(t, j, 0) * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else if constexpr (kVec) {
+    const int off = column<TPR, true>(t, j, 0) * 4;
+    const u32x4 lo = load16(r, off), hi = load16(r, off + 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(lo[i]);
+      v[4 + i] = __uint_as_float(hi[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int off = r.skip + column<TPR, false>(t, j, i) * static_cast<int>(sizeof(T));
+      if constexpr (sizeof(T) == 2)
+        v[i] = bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r.rsrc, off, 0, 0));
+      else
+        v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, off, 0, 0));
+    }
+  }
+}
+template <typename T, int TPR, bool kVec>
+__device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)[8]) {
+  if constexpr (kVec && sizeof(T) == 2) {
+    const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, column<TPR, true>(t, j, 0) * 2, 0, 0);
+  } else if constexpr (kVec) {
+    const int off = column<TPR, true>(t, j, 0) * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 w = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                       __float_as_uint(v[4 * h + 3])};
+      __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, off + 16 * h, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int off = r.skip + column<TPR, false>(t, j, i) * static_cast<int>(sizeof(T));
+      if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[i]), r.rsrc, off, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r.rsrc, off, 0, 0);
+    }
+  }
+}
+// Parameters of either type.
+template <int TPR, bool kVec>
+__device__ __forceinline__ void fetch_param(const void* p, bool bf16, int cols, int t, int j, float (&v)[8]) {
+  if (bf16)
+    fetch<uint16_t, TPR, kVec>(row_at(p, 0, cols * 2), t, j, v);
+  else
+    fetch<float, TPR, kVec>(row_at(p, 0, cols * 4), t, j, v);
+}
+
+template <int TPR>
+constexpr int kBlockThreads = TPR == 64 ? 256 : TPR;
+
+template <typename T, int TPR, int NC, bool kVec>
+__global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(const NormFwdLaunch a) {
+  constexpr int kRows = kBlockThreads<TPR> / TPR;
+  __shared__ float part[2 * TPR / 64];
+  const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  const float count = static_cast<float>(cols);
+  const int blocks = (cols + kAct8Block - 1) / kAct8Block;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
+    const Row x = row_at(a.x, row * row_bytes, row_bytes);
+    float v[NC][8];
+    float sum = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) fetch<T, TPR, kVec>(x, t, j, v[j]);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[j][i];
+    row_sum2<TPR>(sum, none, part);
+    const float near = sum / count;  // the mean, within the rounding of the sum
+    float sq = 0.0f, off = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[j][i] = column<TPR, kVec>(t, j, i) < cols ? v[j][i] - near : 0.0f;
+        off += v[j][i];
+        sq = fmaf(v[j][i], v[j][i], sq);
+      }
+    row_sum2<TPR>(sq, off, part);
+    off /= count;  // what `near` missed
+    const float mean = near + off;
+    const float rstd = 1.0f / sqrtf(fmaxf(sq / count - off * off, 0.0f) + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    const Row y = row_at(a.y, row * row_bytes, row_bytes);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = v[j][i] = (v[j][i] - off) * rstd;
+      float p[8];
+      if (a.weight) {
+        fetch_param<TPR, kVec>(a.weight, a.param_bf16, cols, t, j, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= p[i];
+      }
+      if (a.bias) {
+        fetch_param<TPR, kVec>(a.bias, a.param_bf16, cols, t, j, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += p[i];
+      }
+      put<T, TPR, kVec>(y, t, j, o);
+      if (a.codes) {
+        const Row codes = row_at(a.codes, row * cols, cols), scale = row_at(a.scale, row * blocks, blocks);
+        if constexpr (kVec) {
+          const int c = column<TPR, true>(t, j, 0);
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = max(m, act8_mag(v[j][i]));
+          const int e = static_cast<int>(quad_max(m) >> 23);
+          int q[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = act8_encode(v[j][i], e);
+          const u32x2 w = {act8_pack(q[0], q[1], q[2], q[3]), act8_pack(q[4], q[5], q[6], q[7])};
+          __builtin_amdgcn_raw_buffer_store_b64(w, codes.rsrc, c, 0, 0);
+          if ((t & 3) == 0)
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), scale.rsrc, scale.skip + (c >> 5), 0, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = column<TPR, false>(t, j, i);
+            const int e = static_cast<int>(half_wave_max(act8_mag(v[j][i])) >> 23);
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(act8_encode(v[j][i], e)), codes.rsrc,
+                                                 codes.skip + c, 0, 0);
+            if ((t & 31) == 0)
+              __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), scale.rsrc, scale.skip + (c >> 5), 0, 0);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Where a row's xhat comes from: x, mean and rstd, or the 8-bit checkpoint.
+struct XhatRow {
+  Row x, scale;
+  float mean, rstd;
+};
+// 8 entries of xhat; entries past the row are not meant to be used.
+template <typename T, int TPR, bool kVec, bool kAct8>
+__device__ __forceinline__ void fetch_xhat(const XhatRow& r, int t, int j, float (&v)[8]) {
+  if constexpr (!kAct8) {
+    fetch<T, TPR, kVec>(r.x, t, j, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (v[i] - r.mean) * r.rstd;
+  } else if constexpr (kVec) {
+    const int c = column<TPR, true>(t, j, 0);
+    const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r.x.rsrc, c, 0, 0);
+    const int e = __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, r.scale.skip + (c >> 5), 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act8_decode(act8_byte(w[i >> 2], i & 3), e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<TPR, false>(t, j, i);
+      const int8_t q = static_cast<int8_t>(__builtin_amdgcn_raw_buffer_load_b8(r.x.rsrc, r.x.skip + c, 0, 0));
+      v[i] = act8_decode(q, __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, r.scale.skip + (c >> 5), 0, 0));
+    }
+  }
+}
+
+__device__ __forceinline__ XhatRow xhat_row(const NormBwdLaunch& a, int64_t row, int row_bytes, bool act8) {
+  XhatRow r;
+  r.rstd = a.rstd[row];
+  if (act8) {
+    const int blocks = (a.cols + kAct8Block - 1) / kAct8Block;
+    r.mean = 0.0f;
+    r.x = row_at(a.codes, row * a.cols, a.cols);
+    r.scale = row_at(a.scale, row * blocks, blocks);
+  } else {
+    r.mean = a.mean[row];
+    r.x = row_at(a.x, row * row_bytes, row_bytes);
+  }
+  return r;
+}
+
+// kParams: with the column sums.  Without them it is the dx of the widest rows
+// (and of calls that ask for dx alone), whose sums have a kernel of their own.
+template <typename T, int TPR, int NC, bool kVec, bool kAct8, bool kParams>
+__global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(const NormBwdLaunch a) {
+  constexpr int kRows = kBlockThreads<TPR> / TPR;
+  constexpr int kSums = kParams && kRows > 1 ? 2 * 8 * NC * TPR : 1;
+  constexpr int kHeld = kParams ? NC : 1;
+  __shared__ float part[2 * TPR / 64];
+  __shared__ float sums[kSums];  // [2][8 NC TPR], the rows of a workgroup joined one after the other
+  const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  const float inv = 1.0f / static_cast<float>(cols);
+  float dw[kHeld][8], db[kHeld][8], w[kHeld][8];
+  auto weight = [&](int j, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+    if (a.weight) fetch_param<TPR, kVec>(a.weight, a.param_bf16, cols, t, j, v);
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = db[j][i] = 0.0f;
+    if constexpr (kParams) weight(j, w[j]);
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
+    const Row dy = row_at(a.dy, row * row_bytes, row_bytes);
+    const XhatRow xr = xhat_row(a, row, row_bytes, kAct8);
+    float g[NC][8], xh[NC][8];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      fetch<T, TPR, kVec>(dy, t, j, g[j]);
+      fetch_xhat<T, TPR, kVec, kAct8>(xr, t, j, xh[j]);
+    }
+    // Places past the row count as zero.
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int held = kParams ? j : 0;
+      if constexpr (!kParams) weight(j, w[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = column<TPR, kVec>(t, j, i) < cols;
+        const float d = g[j][i], x = in ? xh[j][i] : 0.0f;
+        if constexpr (kParams) {
+          dw[j][i] = fmaf(d, x, dw[j][i]);
+          db[j][i] += d;
+        }
+        const float y = d * w[held][i];
+        xh[j][i] = x;
+        g[j][i] = y;
+        s1 += in ? y : 0.0f;
+        s2 = fmaf(y, x, s2);
+      }
+    }
+    row_sum2<TPR>(s1, s2, part);
+    s1 *= inv;
+    s2 *= inv;
+    if (a.dx) {
+      const Row dx = row_at(a.dx, row * row_bytes, row_bytes);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = (g[j][i] - s1 - xh[j][i] * s2) * xr.rstd;
+        put<T, TPR, kVec>(dx, t, j, o);
+      }
+    }
+  }
+  if constexpr (kParams) {
+    if constexpr (kRows > 1) {
+      for (int r = 0; r < kRows; ++r) {
+        if (sub == r) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int s = (8 * j + i) * TPR + t;
+              sums[s] = r == 0 ? dw[j][i] : sums[s] + dw[j][i];
+              sums[8 * NC * TPR + s] = r == 0 ? db[j][i] : sums[8 * NC * TPR + s] + db[j][i];
+            }
+        }
+        __syncthreads();
+      }
+      if (sub != 0) return;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = (8 * j + i) * TPR + t;
+          dw[j][i] = sums[s];
+          db[j][i] = sums[8 * NC * TPR + s];
+        }
+    }
+    float* ws = a.workspace + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    const Row wdw = row_at(ws, 0, cols * 4), wdb = row_at(ws + cols, 0, cols * 4);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      put<float, TPR, kVec>(wdw, t, j, dw[j]);
+      put<float, TPR, kVec>(wdb, t, j, db[j]);
+    }
+  }
+}
+
+// The column sums alone: workgroup (x, y) takes columns 2048 x ... and rows y,
+// y + gridDim.y, ...  For rows too wide for quest_norm_bwd_kernel to hold
+// their sums beside their entries, at the price of a second read.
+template <typename T, bool kVec, bool kAct8>
+__global__ void __launch_bounds__(256) quest_norm_colsum_kernel(const NormBwdLaunch a) {
+  const int t = threadIdx.x, j = blockIdx.x;
+  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  float dw[8] = {}, db[8] = {};
+#pragma unroll 2
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    float g[8], xh[8];
+    fetch<T, 256, kVec>(row_at(a.dy, row * row_bytes, row_bytes), t, j, g);
+    fetch_xhat<T, 256, kVec, kAct8>(xhat_row(a, row, row_bytes, kAct8), t, j, xh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] = fmaf(g[i], xh[i], dw[i]);
+      db[i] += g[i];
+    }
+  }
+  float* ws = a.workspace + static_cast<int64_t>(blockIdx.y) * 2 * cols;
+  put<float, 256, kVec>(row_at(ws, 0, cols * 4), t, j, dw);
+  put<float, 256, kVec>(row_at(ws + cols, 0, cols * 4), t, j, db);
+}
+
+// The workgroups' column sums added in a fixed order: thread (s, c) of a
+// workgroup adds every 4th of them from s for column c, then the four.
+template <typename P>
+__global__ void __launch_bounds__(256)
+    quest_norm_params_kernel(const float* __restrict__ ws, int groups, int cols, P* __restrict__ dw,
+                             P* __restrict__ db) {
+  __shared__ float part[4][64];
+  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;  // column of [dw | db]
+  float v = 0.0f;
+  if (c < 2 * cols)
+    for (int g = s; g < groups; g += 4) v += ws[static_cast<int64_t>(g) * 2 * cols + c];
+  part[s][lane] = v;
+  __syncthreads();
+  if (s != 0 || c >= 2 * cols) return;
+  v = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  if (c < cols) {
+    if (dw) dw[c] = from_f32<P>(v);
+  } else if (db) {
+    db[c - cols] = from_f32<P>(v);
+  }
+}
+
+constexpr int kMaxFwdBlocks = 1 << 20;  // more rows are walked
+constexpr int kMaxHeldCols = 16384;      // widest rows whose backward holds entries and column sums in registers
+
+template <typename T, int TPR, int NC, bool kVec>
+hipError_t fwd(const NormFwdLaunch& a) {
+  constexpr int kRows = kBlockThreads<TPR> / TPR;
+  const int64_t n = (a.rows + kRows - 1) / kRows;
+  hipLaunchKernelGGL((quest_norm_fwd_kernel<T, TPR, NC, kVec>),
+                     dim3(static_cast<uint32_t>(n < kMaxFwdBlocks ? n : kMaxFwdBlocks)), dim3(kBlockThreads<TPR>), 0,
+                     a.stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kVec>
+hipError_t fwd_width(const NormFwdLaunch& a) {
+  if (a.cols <= 512) return fwd<T, 64, 1, kVec>(a);
+  if (a.cols <= 1024) return fwd<T, 64, 2, kVec>(a);
+  if (a.cols <= 2048) return fwd<T, 64, 4, kVec>(a);
+  if (a.cols <= 4096) return fwd<T, 256, 2, kVec>(a);
+  if (a.cols <= 8192) return fwd<T, 256, 4, kVec>(a);
+  if (a.cols <= 16384) return fwd<T, 1024, 2, kVec>(a);
+  return fwd<T, 1024, 4, kVec>(a);
+}
+
+template <typename T, int TPR, int NC, bool kVec, bool kParams>
+hipError_t bwd(const NormBwdLaunch& a, int groups) {
+  if (a.codes)
+    hipLaunchKernelGGL((quest_norm_bwd_kernel<T, TPR, NC, kVec, true, kParams>), dim3(groups),
+                       dim3(kBlockThreads<TPR>), 0, a.stream, a);
+  else
+    hipLaunchKernelGGL((quest_norm_bwd_kernel<T, TPR, NC, kVec, false, kParams>), dim3(groups),
+                       dim3(kBlockThreads<TPR>), 0, a.stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kVec>
+hipError_t bwd_width(const NormBwdLaunch& a, int groups) {
+  if (a.workspace && a.cols > kMaxHeldCols) {
+    const dim3 grid((a.cols + 2047) / 2048, groups);
+    if (a.codes)
+      hipLaunchKernelGGL((quest_norm_colsum_kernel<T, kVec, true>), grid, dim3(256), 0, a.stream, a);
+    else
+      hipLaunchKernelGGL((quest_norm_colsum_kernel<T, kVec, false>), grid, dim3(256), 0, a.stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dx) return e;
+  } else if (a.workspace) {
+    if (a.cols <= 512) return bwd<T, 64, 1, kVec, true>(a, groups);
+    if (a.cols <= 1024) return bwd<T, 64, 2, kVec, true>(a, groups);
+    if (a.cols <= 2048) return bwd<T, 64, 4, kVec, true>(a, groups);
+    if (a.cols <= 4096) return bwd<T, 256, 2, kVec, true>(a, groups);
+    if (a.cols <= 8192) return bwd<T, 256, 4, kVec, true>(a, groups);
+    return bwd<T, 512, 4, kVec, true>(a, groups);
+  }
+  // dx alone: rows in workgroups of their own, as the forward
+  const int64_t n = a.cols <= 2048 ? (a.rows + 3) / 4 : a.rows;
+  groups = static_cast<int>(n < kMaxFwdBlocks ? n : kMaxFwdBlocks);
+  if (a.cols <= 512) return bwd<T, 64, 1, kVec, false>(a, groups);
+  if (a.cols <= 2048) return bwd<T, 64, 4, kVec, false>(a, groups);
+  if (a.cols <= 8192) return bwd<T, 256, 4, kVec, false>(a, groups);
+  return bwd<T, 1024, 4, kVec, false>(a, groups);
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16) {
+  const bool vec = a.cols % 8 == 0;
+  if (x_bf16) return vec ? fwd_width<uint16_t, true>(a) : fwd_width<uint16_t, false>(a);
+  return vec ? fwd_width<float, true>(a) : fwd_width<float, false>(a);
+}
+
+int norm_bwd_groups(int64_t rows, int64_t cols) {
+  const int64_t per = cols <= 2048 ? 4 : 1;  // rows a workgroup holds at a time
+  const int64_t n = (rows + per - 1) / per;
+  return static_cast<int>(n < 512 ? n : 512);
+}
+
+hipError_t launch_norm_bwd(const NormBwdLaunch& a, bool bf16) {
+  const int groups = norm_bwd_groups(a.rows, a.cols);
+  if (groups > 0) {
+    const bool vec = a.cols % 8 == 0;
+    const hipError_t e = bf16 ? (vec ? bwd_width<uint16_t, true>(a, groups) : bwd_width<uint16_t, false>(a, groups))
+                              : (vec ? bwd_width<float, true>(a, groups) : bwd_width<float, false>(a, groups));
+    if (e != hipSuccess) return e;
+  }
+  if (a.dweight || a.dbias) {
+    const dim3 grid((2 * a.cols + 63) / 64);
+    if (a.param_bf16)
+      hipLaunchKernelGGL(quest_norm_params_kernel<uint16_t>, grid, dim3(256), 0, a.stream, a.workspace, groups,
+                         a.cols, static_cast<uint16_t*>(a.dweight), static_cast<uint16_t*>(a.dbias));
+    else
+      hipLaunchKernelGGL(quest_norm_params_kernel<float>, grid, dim3(256), 0, a.stream, a.workspace, groups, a.cols,
+                         static_cast<float*>(a.dweight), static_cast<float*>(a.dbias));
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace quest
