@@ -660,14 +660,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without making a torch.cuda.Stream of it (a tenth of the time), where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch(call: str, dev: torch.device, stream, *args) -> None:
     """One device call of the library on `stream` (default: dev's current stream), with dev the current device."""
     fn = getattr(load_library(), call)
+    handle = _raw_stream(dev.index) if stream is None and _raw_stream else _stream_handle(dev, stream)
     if torch.cuda.current_device() == dev.index:
-        _check(call, fn(*args, _stream_handle(dev, stream)))
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(call, fn(*args, _stream_handle(dev, stream)))
+            status = fn(*args, handle)
+    if status != QUEST_OK:
+        _check(call, status)
 
 
 def _matrix(name: str, t) -> None:
@@ -682,18 +689,31 @@ def _exactly(name: str, t, dtype, shape) -> None:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _act8_pair(name: str, pair, rows: int, cols: int):
-    """(codes, scale) of an 8-bit checkpoint of a rows x cols tensor."""
+def _check_tensors(dev: torch.device, *specs) -> None:
+    """Every (name, tensor, dtype, shape) of that type and shape (a number: at least so many elements),
+    contiguous and on the GPU `dev`.  Types and sizes are checked before any device; the loop that finds
+    everything in order is kept short, since small calls cost what the host does."""
+    for _, t, dtype, shape in specs:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_cuda
+                and t.is_contiguous() and (t.numel() >= shape if type(shape) is int else t.shape == shape)):
+            break
+    else:
+        return
+    for name, t, dtype, shape in specs:
+        (_buffer if type(shape) is int else _exactly)(name, t, dtype, shape)
+    _on_device(dev, **{name: t for name, t, _, _ in specs})
+
+
+def _act8_specs(name: str, pair, rows: int, cols: int):
+    """What the (codes, scale) of a rows x cols tensor's 8-bit checkpoint have to be, for _check_tensors."""
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise TypeError(f"{name} must be the (codes, scale) pair of an 8-bit checkpoint")
-    codes, scale = pair
-    _exactly(f"{name} codes", codes, torch.int8, (rows, cols))
-    _exactly(f"{name} scale", scale, torch.uint8, (rows, -(-cols // 32)))
-    return codes, scale
+    return ((f"{name} codes", pair[0], torch.int8, (rows, cols)),
+            (f"{name} scale", pair[1], torch.uint8, (rows, -(-cols // 32))))
 
 
 def _new_act8(rows: int, cols: int, device):
@@ -709,13 +729,13 @@ def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
     """
     _matrix("x", x)
     rows, cols = x.shape
+    dev = x.device
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
     if scale is None:
-        scale = torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=x.device)
-    _act8_pair("the checkpoint's", (codes, scale), rows, cols)
-    _on_device(x.device, x=x, codes=codes, scale=scale)
-    _launch("quest_act8_save", x.device, stream, x.data_ptr(), _dtype_code(x), rows, cols, codes.data_ptr(),
+        scale = torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=dev)
+    _check_tensors(dev, ("x", x, x.dtype, x.shape), *_act8_specs("the checkpoint's", (codes, scale), rows, cols))
+    _launch("quest_act8_save", dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, codes.data_ptr(),
             scale.data_ptr())
     return codes, scale
 
@@ -726,29 +746,30 @@ def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError("codes must be a 2-D tensor (rows x cols)")
     rows, cols = codes.shape
-    _act8_pair("the checkpoint's", (codes, scale), rows, cols)
+    dev = codes.device
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
     _matrix("out", out)
-    _exactly("out", out, out.dtype, (rows, cols))
-    _on_device(codes.device, codes=codes, scale=scale, out=out)
-    _launch("quest_act8_load", codes.device, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(),
+    _check_tensors(dev, *_act8_specs("the checkpoint's", (codes, scale), rows, cols),
+                   ("out", out, out.dtype, (rows, cols)))
+    _launch("quest_act8_load", dev, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(),
             _dtype_code(out))
     return out
 
 
 def _norm_params(cols: int, weight, bias):
-    """The tensors among weight and bias by name, and their common type's code."""
-    given = {k: t for k, t in (("weight", weight), ("bias", bias)) if t is not None}
-    code = QUEST_F32
-    for name, t in given.items():
+    """_check_tensors' entries for those of weight and bias that are given, and their common type's code."""
+    specs, code = (), QUEST_F32
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
+        if specs and t.dtype != specs[0][2]:
+            raise TypeError(f"weight and bias must share one type, got {weight.dtype} and {bias.dtype}")
         code = _dtype_code(t)
-        _exactly(name, t, t.dtype, (cols,))
-    if len(given) == 2 and weight.dtype != bias.dtype:
-        raise TypeError(f"weight and bias must share one type, got {weight.dtype} and {bias.dtype}")
-    return given, code
+        specs += ((name, t, t.dtype, (cols,)),)
+    return specs, code
 
 
 def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, act8: bool = False, out=None,
@@ -763,13 +784,12 @@ def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, a
     _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
-    given, param_code = _norm_params(cols, weight, bias)
+    params, param_code = _norm_params(cols, weight, bias)
     if out is None:
         out = torch.empty_like(x)
-    _exactly("out", out, x.dtype, (rows, cols))
-    _on_device(dev, x=x, out=out, **given)
+    _check_tensors(dev, ("x", x, x.dtype, x.shape), ("out", out, x.dtype, x.shape), *params)
     mean = torch.empty((rows,), dtype=torch.float32, device=dev)
-    rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
     codes, scale = _new_act8(rows, cols, dev) if act8 else (None, None)
     _launch("quest_layer_norm_fwd", dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ptr(weight), _ptr(bias),
             param_code, float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(codes), _ptr(scale))
@@ -795,20 +815,17 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
         raise ValueError("no gradient is asked for")
     if (act8 is None) == (x is None) or (x is None) != (mean is None):
         raise ValueError("give x and mean, or act8")
-    given, _ = _norm_params(cols, weight, None)
-    _exactly("rstd", rstd, torch.float32, (rows,))
-    codes = scale = None
+    params, _ = _norm_params(cols, weight, None)
     if act8 is None:
-        _exactly("x", x, dy.dtype, (rows, cols))
-        _exactly("mean", mean, torch.float32, (rows,))
-        given.update(x=x, mean=mean)
+        codes = scale = None
+        source = (("x", x, dy.dtype, dy.shape), ("mean", mean, torch.float32, (rows,)))
     else:
-        codes, scale = _act8_pair("act8", act8, rows, cols)
-        given.update(codes=codes, scale=scale)
+        source = _act8_specs("act8", act8, rows, cols)
+        codes, scale = act8
     param_dtype = weight.dtype if weight is not None else param_dtype or torch.float32
     if param_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"parameter gradients are float32 or bfloat16, not {param_dtype}")
-    _on_device(dev, dy=dy, rstd=rstd, **given)
+    _check_tensors(dev, ("dy", dy, dy.dtype, dy.shape), ("rstd", rstd, torch.float32, (rows,)), *source, *params)
     dx = torch.empty_like(dy) if input_grad else None
     dweight = torch.empty((cols,), dtype=param_dtype, device=dev) if weight_grad else None
     dbias = torch.empty((cols,), dtype=param_dtype, device=dev) if bias_grad else None
@@ -843,16 +860,17 @@ def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate:
     """
     n, m, k = int(n), int(m), int(k)
     code = _act_code(act)
-    for name, t, rows in (("x", x, n), ("gate", gate, m), ("up", up, m)):
-        _buffer(name, t, torch.uint8, operand_bytes(rows, k))
-    for name, t, rows in (("x_scale", x_scale, n), ("gate_scale", gate_scale, m), ("up_scale", up_scale, m)):
-        _buffer(name, t, torch.float32, rows)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
     dev = x.device
     if out is None:
         out = torch.empty((n, m), dtype=out_dtype, device=dev)
     _matrix("out", out)
-    _exactly("out", out, out.dtype, (n, m))
-    _on_device(dev, x=x, x_scale=x_scale, gate=gate, gate_scale=gate_scale, up=up, up_scale=up_scale, out=out)
+    nx, nw = operand_bytes(n, k), operand_bytes(m, k)
+    _check_tensors(dev, ("x", x, torch.uint8, nx), ("x_scale", x_scale, torch.float32, n),
+                   ("gate", gate, torch.uint8, nw), ("gate_scale", gate_scale, torch.float32, m),
+                   ("up", up, torch.uint8, nw), ("up_scale", up_scale, torch.float32, m),
+                   ("out", out, out.dtype, (n, m)))
     gate8 = _new_act8(n, m, dev) if act8 else (None, None)
     up8 = _new_act8(n, m, dev) if act8 else (None, None)
     _launch("quest_gated_fwd", dev, stream, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
@@ -869,13 +887,12 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
     """
     _matrix("dh", dh)
     rows, cols = dh.shape
+    dev = dh.device
     code = _act_code(act)
-    gc, gs = _act8_pair("gate8", gate8, rows, cols)
-    uc, us = _act8_pair("up8", up8, rows, cols)
     if out is None:
-        out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dh.device)
-    _exactly("out", out, dh.dtype, (rows, 2 * cols))
-    _on_device(dh.device, dh=dh, gate_codes=gc, gate_scale=gs, up_codes=uc, up_scale=us, out=out)
-    _launch("quest_gated_bwd", dh.device, stream, dh.data_ptr(), _dtype_code(dh), rows, cols, gc.data_ptr(),
-            gs.data_ptr(), uc.data_ptr(), us.data_ptr(), code, out.data_ptr())
+        out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dev)
+    _check_tensors(dev, ("dh", dh, dh.dtype, dh.shape), *_act8_specs("gate8", gate8, rows, cols),
+                   *_act8_specs("up8", up8, rows, cols), ("out", out, dh.dtype, (rows, 2 * cols)))
+    _launch("quest_gated_bwd", dev, stream, dh.data_ptr(), _dtype_code(dh), rows, cols, gate8[0].data_ptr(),
+            gate8[1].data_ptr(), up8[0].data_ptr(), up8[1].data_ptr(), code, out.data_ptr())
     return out

@@ -64,6 +64,82 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// The same at any address that is a multiple of the element's size (global
+// memory takes wide accesses there at no more than the lines they touch), for
+// the `left` entries that a row has from there: 8 or more, a row's last few,
+// entry by entry (the others read as zero), or none.
+template <typename T>
+__device__ __forceinline__ void load8_tail(const T* p, int left, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (left >= 8) {
+    typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+    const u32x4_u a = *reinterpret_cast<const u32x4_u*>(p);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(a[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      }
+    } else {
+      const u32x4_u b = *reinterpret_cast<const u32x4_u*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(a[i]);
+        v[4 + i] = __uint_as_float(b[i]);
+      }
+    }
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) v[i] = to_f32(p[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8_tail(T* p, int left, const float (&v)[8]) {
+  if (left >= 8) {
+    typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4_u*>(p) =
+          u32x4_u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4_u*>(p + 4 * h) =
+            u32x4_u{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                    __float_as_uint(v[4 * h + 3])};
+    }
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) p[i] = from_f32<T>(v[i]);
+  }
+}
+// 8 codes likewise.
+__device__ __forceinline__ uint2 load_codes8_tail(const int8_t* p, int left) {
+  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
+  uint2 w = make_uint2(0, 0);
+  if (left >= 8) {
+    const u32x2_u a = *reinterpret_cast<const u32x2_u*>(p);
+    w = make_uint2(a[0], a[1]);
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) (i < 4 ? w.x : w.y) |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3));
+  }
+  return w;
+}
+__device__ __forceinline__ void store_codes8_tail(int8_t* p, int left, uint2 w) {
+  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
+  if (left >= 8) {
+    *reinterpret_cast<u32x2_u*>(p) = u32x2_u{w.x, w.y};
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) p[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+  }
+}
+
 // The magnitude's bit pattern: ordered as the magnitudes, NaN above infinity.
 __device__ __forceinline__ uint32_t act8_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
@@ -85,15 +161,41 @@ __device__ __forceinline__ uint32_t act8_pack(int a, int b, int c, int d) {
 }
 __device__ __forceinline__ int act8_byte(uint32_t w, int i) { return static_cast<int8_t>(w >> (8 * i)); }
 
-// max over the lanes of an aligned group of 4 (quad) or 32 lanes.
+// 8 entries encoded and decoded.
+__device__ __forceinline__ uint2 act8_encode8(const float (&v)[8], int e) {
+  int q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = act8_encode(v[i], e);
+  return make_uint2(act8_pack(q[0], q[1], q[2], q[3]), act8_pack(q[4], q[5], q[6], q[7]));
+}
+__device__ __forceinline__ void act8_decode8(uint2 w, int e, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = act8_decode(act8_byte(i < 4 ? w.x : w.y, i & 3), e);
+}
+__device__ __forceinline__ uint32_t act8_mag8(const float (&v)[8]) {
+  uint32_t a = act8_mag(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = max(a, act8_mag(v[i]));
+  return a;
+}
+
+// max over the lanes of an aligned group of 4 (quad) or 32 lanes (half wave).
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, true)));
   return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, true)));
 }
+// (v_permlane16_swap_b32 of a value with itself leaves rows 0 0 2 2 and 1 1 3 3
+// of 16 lanes, v_permlane32_swap_b32 halves 0 0 and 1 1.)
 __device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d, 64)));
-  return v;
+  v = quad_max(v);
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x141, 0xF, 0xF, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x140, 0xF, 0xF, true)));
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max(r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t halves_max(uint32_t v) {  // of lanes l and l ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(r[0], r[1]);
 }
 
 }  // namespace quest

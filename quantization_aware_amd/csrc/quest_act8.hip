@@ -3,10 +3,13 @@
 //
 // Both are one pass over memory with a few operations an entry: bound by HBM.
 // Rows of whole blocks (cols a multiple of 32) are one stretch of memory, in
-// which entry 8 t .. 8 t + 7 of the tensor belongs to lane t: 16-byte
-// accesses of bf16, 8-byte accesses of codes, and a block is four
-// neighbouring lanes, whose maximum is two DPP steps.  Other widths go a row
-// per wave, an entry per lane, a block per half wave.
+// which entries 8 t .. 8 t + 7 belong to thread t: 16-byte accesses of bf16,
+// 8-byte accesses of codes, and a block is four neighbouring lanes, whose
+// maximum is two DPP steps.  Other widths keep those accesses at unaligned
+// addresses, four lanes a block, a row's last entries one by one; a workgroup
+// takes a run of consecutive blocks of the tensor, whatever rows they are of,
+// so narrow rows fill the waves as well as wide ones.  (8192 x 1001 bf16 is
+// saved in 8.4 us and read in 6.0; an entry an access took 12.5 and 10.6.)
 #include "quest_act8.h"
 
 #include "quest_launch.h"
@@ -15,17 +18,24 @@ namespace quest {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRowBlocks = 1 << 20;  // workgroups of the row-per-wave kernels, which walk the rows beyond
 constexpr int kUnroll = 4;  // groups of 8 entries a thread handles in one pass, their loads together
 
-__device__ __forceinline__ int64_t first_row() {
-  return static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-}
-__device__ __forceinline__ int64_t row_stride() { return static_cast<int64_t>(gridDim.x) * (kThreads / 64); }
-uint32_t row_blocks(int64_t rows) {
-  const int64_t n = (rows + kThreads / 64 - 1) / (kThreads / 64);
-  return static_cast<uint32_t>(n < kMaxRowBlocks ? n : kMaxRowBlocks);
-}
+// Block number `first` + i of the tensor as (row, block of the row), for a
+// workgroup's first block (a 64-bit division, once and uniform) and small i.
+struct BlockRun {
+  int64_t row;
+  uint32_t rem, blocks;
+  __device__ __forceinline__ BlockRun(int64_t first, int cols)
+      : blocks(static_cast<uint32_t>(cols + kAct8Block - 1) / kAct8Block) {
+    row = first / blocks;
+    rem = static_cast<uint32_t>(first - row * blocks);
+  }
+  __device__ __forceinline__ void at(uint32_t i, int64_t& r, int& b) const {
+    const uint32_t t = rem + i, q = t / blocks;
+    r = row + q;
+    b = static_cast<int>(t - q * blocks);
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -42,45 +52,40 @@ __global__ void __launch_bounds__(kThreads)
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t g = base + u * kThreads;
     if (g >= groups) break;  // groups is a multiple of 4: a block's lanes stay together
-    uint32_t a = act8_mag(v[u][0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a = max(a, act8_mag(v[u][i]));
-    const int e = static_cast<int>(quad_max(a) >> 23);
-    int q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = act8_encode(v[u][i], e);
-    *reinterpret_cast<uint2*>(codes + 8 * g) =
-        make_uint2(act8_pack(q[0], q[1], q[2], q[3]), act8_pack(q[4], q[5], q[6], q[7]));
+    const int e = static_cast<int>(quad_max(act8_mag8(v[u])) >> 23);
+    *reinterpret_cast<uint2*>(codes + 8 * g) = act8_encode8(v[u], e);
     if ((g & 3) == 0) scale[g >> 2] = static_cast<uint8_t>(e);
   }
 }
 
+constexpr int kRun = kThreads / 4;  // blocks at a time
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    quest_act8_save_rows_kernel(const T* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ codes,
-                                uint8_t* __restrict__ scale) {
-  const int lane = threadIdx.x & 63;
-  const int blocks = (cols + kAct8Block - 1) / kAct8Block;
-  for (int64_t row = first_row(); row < rows; row += row_stride()) {
-    const T* xr = x + row * cols;
-    int8_t* cr = codes + row * cols;
-    uint8_t* sr = scale + row * blocks;
-    for (int c0 = 0; c0 < cols; c0 += 64 * kUnroll) {
-      float v[kUnroll];
+    quest_act8_save_blocks_kernel(const T* __restrict__ x, int64_t total, int cols, int8_t* __restrict__ codes,
+                                  uint8_t* __restrict__ scale) {
+  const int l = threadIdx.x % 4, sub = threadIdx.x / 4;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRun * kUnroll); first < total;
+       first += static_cast<int64_t>(gridDim.x) * (kRun * kUnroll)) {
+    const BlockRun run(first, cols);
+    float v[kUnroll][8];
+    int64_t at[kUnroll];
+    int left[kUnroll];  // entries of the row from there
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int c = c0 + 64 * u + lane;
-        v[u] = c < cols ? to_f32(xr[c]) : 0.0f;
-      }
+    for (int u = 0; u < kUnroll; ++u) {
+      int64_t r;
+      int b;
+      run.at(u * kRun + sub, r, b);
+      const int c = b * kAct8Block + 8 * l;
+      left[u] = first + u * kRun + sub < total ? cols - c : 0;
+      at[u] = r * cols + c;
+      load8_tail(x + at[u], left[u], v[u]);
+    }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int c = c0 + 64 * u + lane;
-        const int e = static_cast<int>(half_wave_max(act8_mag(v[u])) >> 23);
-        if (c < cols) {
-          cr[c] = static_cast<int8_t>(act8_encode(v[u], e));
-          if ((lane & 31) == 0) sr[c >> 5] = static_cast<uint8_t>(e);
-        }
-      }
+    for (int u = 0; u < kUnroll; ++u) {
+      const int e = static_cast<int>(quad_max(act8_mag8(v[u])) >> 23);
+      store_codes8_tail(codes + at[u], left[u], act8_encode8(v[u], e));
+      if (l == 0 && left[u] > 0) scale[first + u * kRun + sub] = static_cast<uint8_t>(e);
     }
   }
 }
@@ -105,47 +110,70 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t g = base + u * kThreads;
     if (g >= groups) break;
     float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act8_decode(act8_byte(i < 4 ? w[u].x : w[u].y, i & 3), e[u]);
+    act8_decode8(w[u], e[u], v);
     store8(out + 8 * g, v);
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    quest_act8_load_rows_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scale, int64_t rows,
-                                int cols, T* __restrict__ out) {
-  const int lane = threadIdx.x & 63;
-  const int blocks = (cols + kAct8Block - 1) / kAct8Block;
-  for (int64_t row = first_row(); row < rows; row += row_stride()) {
-#pragma unroll 4
-    for (int c = lane; c < cols; c += 64)
-      out[row * cols + c] = from_f32<T>(act8_decode(codes[row * cols + c], scale[row * blocks + (c >> 5)]));
+    quest_act8_load_blocks_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scale, int64_t total,
+                                  int cols, T* __restrict__ out) {
+  const int l = threadIdx.x % 4, sub = threadIdx.x / 4;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRun * kUnroll); first < total;
+       first += static_cast<int64_t>(gridDim.x) * (kRun * kUnroll)) {
+    const BlockRun run(first, cols);
+    uint2 w[kUnroll];
+    int e[kUnroll], left[kUnroll];
+    int64_t at[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      int64_t r;
+      int b;
+      run.at(u * kRun + sub, r, b);
+      const int c = b * kAct8Block + 8 * l;
+      left[u] = first + u * kRun + sub < total ? cols - c : 0;
+      at[u] = r * cols + c;
+      e[u] = left[u] > 0 ? scale[first + u * kRun + sub] : 0;
+      w[u] = load_codes8_tail(codes + at[u], left[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float v[8];
+      act8_decode8(w[u], e[u], v);
+      store8_tail(out + at[u], left[u], v);
+    }
   }
+}
+
+// Workgroups of the block kernels, at most 2^20 (they walk the blocks beyond).
+uint32_t block_grid(int64_t total) {
+  const int64_t per = kRun * kUnroll, n = (total + per - 1) / per;
+  return static_cast<uint32_t>(n < (1 << 20) ? n : (1 << 20));
 }
 
 template <typename T>
 hipError_t save(const T* x, int64_t rows, int cols, int8_t* codes, uint8_t* scale, hipStream_t stream) {
+  const int64_t total = rows * ((cols + kAct8Block - 1) / kAct8Block);
   if (cols % kAct8Block == 0) {
     const int64_t groups = rows * cols / 8, per = kThreads * kUnroll;
     hipLaunchKernelGGL(quest_act8_save_flat_kernel<T>, dim3(static_cast<uint32_t>((groups + per - 1) / per)),
                        dim3(kThreads), 0, stream, x, groups, codes, scale);
   } else {
-    hipLaunchKernelGGL(quest_act8_save_rows_kernel<T>, dim3(row_blocks(rows)),
-                       dim3(kThreads), 0, stream, x, rows, cols, codes, scale);
+    hipLaunchKernelGGL(quest_act8_save_blocks_kernel<T>, dim3(block_grid(total)), dim3(kThreads), 0, stream, x, total, cols, codes, scale);
   }
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t load(const int8_t* codes, const uint8_t* scale, int64_t rows, int cols, T* out, hipStream_t stream) {
+  const int64_t total = rows * ((cols + kAct8Block - 1) / kAct8Block);
   if (cols % kAct8Block == 0) {
     const int64_t groups = rows * cols / 8, per = kThreads * kUnroll;
     hipLaunchKernelGGL(quest_act8_load_flat_kernel<T>, dim3(static_cast<uint32_t>((groups + per - 1) / per)),
                        dim3(kThreads), 0, stream, codes, scale, groups, out);
   } else {
-    hipLaunchKernelGGL(quest_act8_load_rows_kernel<T>, dim3(row_blocks(rows)),
-                       dim3(kThreads), 0, stream, codes, scale, rows, cols, out);
+    hipLaunchKernelGGL(quest_act8_load_blocks_kernel<T>, dim3(block_grid(total)), dim3(kThreads), 0, stream, codes, scale, total, cols, out);
   }
   return hipGetLastError();
 }

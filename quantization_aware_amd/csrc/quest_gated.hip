@@ -55,6 +55,20 @@ __device__ __forceinline__ void act_both(float g, int act, float& value, float& 
   }
 }
 
+// 16 bytes of LDS to a row's `left` last elements of T at any multiple of T's
+// size: in one store, or the row's last few one by one.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* dst, const uint8_t* src, int left) {
+  typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(1)));
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  if (left >= kPer) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(src);
+    *reinterpret_cast<u32x4_u*>(dst) = v;
+  } else {
+    for (int e = 0; e < left; ++e) dst[e] = reinterpret_cast<const T*>(src)[e];
+  }
+}
+
 template <typename Out, bool kVec, bool kAct8>
 __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a) {
   constexpr int kOut = static_cast<int>(sizeof(Out));
@@ -230,10 +244,8 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
       }
       if constexpr (kAct8) {
         // the block's other 16 columns are in lane ^ 32
-        mg = max(mg, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mg), 32, 64)));
-        mu = max(mu, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mu), 32, 64)));
-        ex[0][jj] = static_cast<int>(mg >> 23);
-        ex[1][jj] = static_cast<int>(mu >> 23);
+        ex[0][jj] = static_cast<int>(halves_max(mg) >> 23);
+        ex[1][jj] = static_cast<int>(halves_max(mu) >> 23);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -254,15 +266,8 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
       if constexpr (kVec) {
         const int off = col < m ? (row * m + col) * kOut : kNowhereOff;
         __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(src), rout, off, 0, 0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const int off = col + e < m ? (row * m + col + e) * kOut : kNowhereOff;
-          if constexpr (kOut == 4)
-            __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t*>(src + 4 * e), rout, off, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t*>(src + 2 * e), rout, off, 0, 0);
-        }
+      } else if (row < rows_left) {
+        store_chunk<Out>(static_cast<Out*>(a.out) + static_cast<int64_t>(row0 + row) * m + col, src, m - col);
       }
     }
     slab_fence();
@@ -290,10 +295,9 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
           if constexpr (kVec) {
             const int off = col < m ? row * m + col : kNowhereOff;
             __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(src), rc, off, 0, 0);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              __builtin_amdgcn_raw_buffer_store_b8(src[e], rc, col + e < m ? row * m + col + e : kNowhereOff, 0, 0);
+          } else if (row < rows_left) {
+            store_chunk<int8_t>((p ? a.up_codes : a.gate_codes) + static_cast<int64_t>(row0 + row) * m + col, src,
+                                m - col);
           }
         }
         // the exponents of block h of the wave's two
@@ -308,12 +312,136 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
   }
 }
 
-// Backward: a row of the checkpoints per workgroup step, 8 columns a thread
-// (kVec, cols a multiple of 8) or one.
+// Few rows (a decode step): the weights are the work, each read once, and a
+// 256 x 128 tile would leave most of the chip without any.  A workgroup takes
+// 16 kCt columns of h and all n <= 16 kT rows; its 8 waves take every 8th chunk
+// of 128 of k, straight from memory into the operand registers of the 16 x 16 x
+// 128 instruction (lane l: row l % 16, run l / 16 of the chunk, 24 bytes), and
+// add their exact sums through LDS.  kCt is 1, which gives the most workgroups,
+// or 2 where the 8-bit checkpoints need blocks of 32 columns in one place.
+// Bound by the latency of one pass over the weights: 1 x 2048 -> 5632 takes 5.4 us
+// (18.4 us with the 256 x 128 tiles), 17.4 MB.
+typedef float v4f __attribute__((ext_vector_type(4)));
+constexpr int kFewWaves = 8;
+
+__device__ __forceinline__ v8i load_run(const uint8_t* p) {
+  typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
+  const u32x4_a8 lo = *reinterpret_cast<const u32x4_a8*>(p);
+  const u32x2 hi = *reinterpret_cast<const u32x2*>(p + 16);
+  return v8i{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
+             static_cast<int>(hi[0]), static_cast<int>(hi[1]), 0, 0};
+}
+
+template <typename Out, int kT, int kCt, bool kAct8>
+__global__ void __launch_bounds__(64 * kFewWaves) quest_gated_few_kernel(const GatedLaunch a) {
+  constexpr int kCols = 16 * kCt, kTile = 16 * kT * kCols;  // outputs of a workgroup
+  __shared__ __attribute__((aligned(16))) float part[kFewWaves][2][kTile];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
+  const int n = a.n, m = a.m, chunks = a.k >> 7;
+  const int64_t rb_bytes = static_cast<int64_t>(chunks) * kBlock;
+  const int col0 = blockIdx.x * kCols;
+  // Byte of run l / 16 of chunk 0 of operand row r.
+  auto run_at = [&](int r) -> int64_t {
+    const int j = lane >> 4;
+    return (r >> 5) * rb_bytes + (j >> 1) * kFrag + (32 * (j & 1) + (r & 31)) * 24;
+  };
+  const uint8_t* px[kT];
+  const uint8_t* pw[2][kCt];
+#pragma unroll
+  for (int t = 0; t < kT; ++t) px[t] = a.x + run_at(min(16 * t + (lane & 15), n - 1));  // rows past n: the last again
+#pragma unroll
+  for (int c = 0; c < kCt; ++c) {
+    const int64_t at = run_at(col0 + 16 * c + (lane & 15));
+    pw[0][c] = a.gate + at;
+    pw[1][c] = a.up + at;
+  }
+  v4f acc[2][kCt][kT];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int c = 0; c < kCt; ++c)
+#pragma unroll
+      for (int t = 0; t < kT; ++t) acc[p][c][t] = v4f{};
+  v8i fw[2][kCt], fx[kT];
+  auto fetch_chunk = [&](int ch) {
+    const int64_t off = static_cast<int64_t>(ch) * kBlock;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int c = 0; c < kCt; ++c) fw[p][c] = load_run(pw[p][c] + off);
+#pragma unroll
+    for (int t = 0; t < kT; ++t) fx[t] = load_run(px[t] + off);
+  };
+  if (wave < chunks) fetch_chunk(wave);
+  for (int ch = wave; ch < chunks; ch += kFewWaves) {
+    v8i w[2][kCt], x[kT];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int c = 0; c < kCt; ++c) w[p][c] = fw[p][c];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) x[t] = fx[t];
+    if (ch + kFewWaves < chunks) fetch_chunk(ch + kFewWaves);
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int c = 0; c < kCt; ++c)
+          acc[p][c][t] =
+              __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[p][c], x[t], acc[p][c][t], 2, 2, 0, 127, 0, 127);
+  }
+  // lane l has row 16 t + l % 16 and columns 16 c + 4 (l / 16) .. + 3
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int c = 0; c < kCt; ++c)
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+        *reinterpret_cast<v4f*>(&part[wave][p][(16 * t + (lane & 15)) * kCols + 16 * c + 4 * (lane >> 4)]) =
+            acc[p][c][t];
+  __syncthreads();
+  const int blocks = (m + 31) >> 5;
+  for (int o = tid; o < kTile; o += 64 * kFewWaves) {
+    const int row = o / kCols, col = col0 + o % kCols;
+    if (!kAct8 && (row >= n || col >= m)) continue;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      g += part[w][0][o];
+      u += part[w][1][o];
+    }
+    const bool in = row < n && col < m;
+    if (in) {
+      const float fx = a.sx[row] * a.kx;
+      g *= fx * (a.sg[col] * a.kw);
+      u *= fx * (a.su[col] * a.kw);
+      static_cast<Out*>(a.out)[static_cast<int64_t>(row) * m + col] =
+          from_f32<Out>(act_value<sizeof(Out) == 2>(g, a.act) * u);
+    }
+    if constexpr (kAct8) {  // a half wave is a row's block of 32 columns
+      const int eg = static_cast<int>(half_wave_max(in ? act8_mag(g) : 0u) >> 23);
+      const int eu = static_cast<int>(half_wave_max(in ? act8_mag(u) : 0u) >> 23);
+      if (in) {
+        const int64_t at = static_cast<int64_t>(row) * m + col, se = static_cast<int64_t>(row) * blocks + (col >> 5);
+        a.gate_codes[at] = static_cast<int8_t>(act8_encode(g, eg));
+        a.up_codes[at] = static_cast<int8_t>(act8_encode(u, eu));
+        if ((lane & 31) == 0) {
+          a.gate_scale[se] = static_cast<uint8_t>(eg);
+          a.up_scale[se] = static_cast<uint8_t>(eu);
+        }
+      }
+    }
+  }
+}
+
+// Backward: 8 columns a thread, a row a workgroup at a time; rows that are no
+// whole 16 bytes at unaligned addresses, the last columns one by one.  A
+// streaming kernel: 8.06 bytes an entry in bf16.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaunch a) {
   const int cols = a.cols, blocks = (cols + kAct8Block - 1) / kAct8Block;
-  constexpr int kPer = kVec ? 8 : 1;
   constexpr bool kFast = sizeof(T) == 2;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* dh = static_cast<const T*>(a.dh) + row * cols;
@@ -323,30 +451,34 @@ __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaun
     const uint8_t* us = a.up_scale + row * blocks;
     T* dg = static_cast<T*>(a.out) + row * 2 * cols;
     T* du = dg + cols;
-    for (int c = threadIdx.x * kPer; c < cols; c += 256 * kPer) {
-      const int eg = gs[c >> 5], eu = us[c >> 5];
+    for (int c = threadIdx.x * 8; c < cols; c += 256 * 8) {
+      const int left = cols - c;
+      float d[8], g[8], u[8];
+      uint2 wg, wu;
       if constexpr (kVec) {
-        float d[8], og[8], ou[8];
         load8(dh + c, d);
-        const uint2 wg = *reinterpret_cast<const uint2*>(gc + c), wu = *reinterpret_cast<const uint2*>(uc + c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float g = act8_decode(act8_byte(i < 4 ? wg.x : wg.y, i & 3), eg);
-          const float u = act8_decode(act8_byte(i < 4 ? wu.x : wu.y, i & 3), eu);
-          float value, slope;
-          act_both<kFast>(g, a.act, value, slope);
-          og[i] = d[i] * u * slope;
-          ou[i] = d[i] * value;
-        }
-        store8(dg + c, og);
-        store8(du + c, ou);
+        wg = *reinterpret_cast<const uint2*>(gc + c);
+        wu = *reinterpret_cast<const uint2*>(uc + c);
       } else {
-        const float d = to_f32(dh[c]);
-        const float g = act8_decode(gc[c], eg), u = act8_decode(uc[c], eu);
+        load8_tail(dh + c, left, d);
+        wg = load_codes8_tail(gc + c, left);
+        wu = load_codes8_tail(uc + c, left);
+      }
+      act8_decode8(wg, gs[c >> 5], g);
+      act8_decode8(wu, us[c >> 5], u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
         float value, slope;
-        act_both<kFast>(g, a.act, value, slope);
-        dg[c] = from_f32<T>(d * u * slope);
-        du[c] = from_f32<T>(d * value);
+        act_both<kFast>(g[i], a.act, value, slope);
+        g[i] = d[i] * u[i] * slope;
+        u[i] = d[i] * value;
+      }
+      if constexpr (kVec) {
+        store8(dg + c, g);
+        store8(du + c, u);
+      } else {
+        store8_tail(dg + c, left, g);
+        store8_tail(du + c, left, u);
       }
     }
   }
@@ -362,6 +494,25 @@ hipError_t launch(const GatedLaunch& g) {
   return hipGetLastError();
 }
 
+template <typename Out, int kT>
+hipError_t launch_few(const GatedLaunch& g) {
+  const dim3 block(64 * kFewWaves);
+  if (g.gate_codes)
+    hipLaunchKernelGGL((quest_gated_few_kernel<Out, kT, 2, true>), dim3((g.m + 31) / 32), block, 0, g.stream, g);
+  else
+    hipLaunchKernelGGL((quest_gated_few_kernel<Out, kT, 1, false>), dim3((g.m + 15) / 16), block, 0, g.stream, g);
+  return hipGetLastError();
+}
+
+template <typename Out>
+hipError_t launch_fwd(const GatedLaunch& g) {
+  if (g.n <= 16) return launch_few<Out, 1>(g);
+  if (g.n <= 32) return launch_few<Out, 2>(g);
+  if (g.n <= 64) return launch_few<Out, 4>(g);
+  // Rows whose chunks of 16 codes and of 16 bytes of output start on 16 bytes.
+  return g.m % 16 == 0 ? launch<Out, true>(g) : launch<Out, false>(g);
+}
+
 template <typename T>
 hipError_t launch_bwd(const GatedBwdLaunch& a) {
   const dim3 grid(static_cast<uint32_t>(a.rows < (1 << 20) ? a.rows : (1 << 20)));
@@ -375,10 +526,7 @@ hipError_t launch_bwd(const GatedBwdLaunch& a) {
 }  // namespace
 
 hipError_t launch_gated_fwd(const GatedLaunch& g, bool out_bf16) {
-  // Rows whose chunks of 16 codes and of 16 bytes of output start on 16 bytes.
-  const bool vec = g.m % 16 == 0;
-  if (out_bf16) return vec ? launch<uint16_t, true>(g) : launch<uint16_t, false>(g);
-  return vec ? launch<float, true>(g) : launch<float, false>(g);
+  return out_bf16 ? launch_fwd<uint16_t>(g) : launch_fwd<float>(g);
 }
 
 hipError_t launch_gated_bwd(const GatedBwdLaunch& a, bool bf16) {

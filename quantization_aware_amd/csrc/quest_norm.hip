@@ -65,95 +65,91 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* part) {
   }
 }
 
-// The columns of thread t of a row's TPR threads: kVec, groups of 8
-// neighbours 8 (t + TPR j); otherwise single columns t + TPR (8 j + i).
-template <int TPR, bool kVec>
-__device__ __forceinline__ int column(int t, int j, int i) {
-  return kVec ? 8 * (t + TPR * j) + i : t + TPR * (8 * j + i);
+// Group j of thread t of a row's TPR threads: 8 neighbouring columns from here.
+template <int TPR>
+__device__ __forceinline__ int column(int t, int j) {
+  return 8 * (t + TPR * j);
 }
 
-// A row (or a parameter vector) as a buffer resource: accesses past its end
-// read zero and write nothing, so no load or store stands behind a branch.  Its
-// base is rounded down to 4 bytes, `skip` is what that leaves in front.
+// A row, or a parameter vector.  kVec (cols a multiple of 8): as a buffer
+// resource, whose accesses past the end read zero and write nothing, so that no
+// load or store stands behind a branch.  Otherwise by address, with the row's
+// last entries one by one.
 struct Row {
   __amdgpu_buffer_rsrc_t rsrc;
-  int skip;
+  uintptr_t at;
+  int cols;
 };
-__device__ __forceinline__ Row row_at(const void* p, int64_t first, int bytes) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(first);
-  const int skip = static_cast<int>(at & 3);
-  return {__builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at - skip), static_cast<short>(0), bytes + skip,
-                                            0x00020000),
-          skip};
+template <typename T>
+__device__ __forceinline__ Row row_at(const void* p, int64_t row, int cols) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * cols) * sizeof(T);
+  return {__builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), static_cast<short>(0),
+                                            cols * static_cast<int>(sizeof(T)), 0x00020000),
+          at, cols};
 }
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ u32x4 load16(const Row& r, int off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, off, 0, 0);
-}
-
-// 8 entries of a row of T from index j of thread t; zeros past its end.
+// 8 entries of a row of T in group j of thread t; zeros past its end.
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void fetch(const Row& r, int t, int j, float (&v)[8]) {
-  if constexpr (kVec && sizeof(T) == 2) {
-    const u32x4 w = load16(r, column<TPR, true>(t, j, 0) * 2);
+  const int c = column<TPR>(t, j);
+  if constexpr (!kVec) {
+    load8_tail(reinterpret_cast<const T*>(r.at) + c, r.cols - c, v);
+  } else if constexpr (sizeof(T) == 2) {
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, c * 2, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(w[i] << 16);
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-  } else if constexpr (kVec) {
-    const int off = column<TPR, true>(t, j, 0) * 4;
-    const u32x4 lo = load16(r, off), hi = load16(r, off + 16);
+  } else {
+    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, c * 4, 0, 0);
+    const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, c * 4 + 16, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = __uint_as_float(lo[i]);
       v[4 + i] = __uint_as_float(hi[i]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int off = r.skip + column<TPR, false>(t, j, i) * static_cast<int>(sizeof(T));
-      if constexpr (sizeof(T) == 2)
-        v[i] = bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r.rsrc, off, 0, 0));
-      else
-        v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, off, 0, 0));
-    }
   }
 }
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)[8]) {
-  if constexpr (kVec && sizeof(T) == 2) {
+  const int c = column<TPR>(t, j);
+  if constexpr (!kVec) {
+    store8_tail(reinterpret_cast<T*>(r.at) + c, r.cols - c, v);
+  } else if constexpr (sizeof(T) == 2) {
     const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-    __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, column<TPR, true>(t, j, 0) * 2, 0, 0);
-  } else if constexpr (kVec) {
-    const int off = column<TPR, true>(t, j, 0) * 4;
+    __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, c * 2, 0, 0);
+  } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const u32x4 w = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
                        __float_as_uint(v[4 * h + 3])};
-      __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, off + 16 * h, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int off = r.skip + column<TPR, false>(t, j, i) * static_cast<int>(sizeof(T));
-      if constexpr (sizeof(T) == 2)
-        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[i]), r.rsrc, off, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r.rsrc, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(w, r.rsrc, c * 4 + 16 * h, 0, 0);
     }
   }
+}
+// The 8-bit checkpoint of such a group: a block is four neighbouring threads.
+template <int TPR, bool kVec>
+__device__ __forceinline__ void put_act8(const Row& codes, const Row& scale, int t, int j, const float (&v)[8]) {
+  const int c = column<TPR>(t, j);
+  const int e = static_cast<int>(quad_max(act8_mag8(v)) >> 23);
+  const uint2 w = act8_encode8(v, e);
+  if constexpr (kVec)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{w.x, w.y}, codes.rsrc, c, 0, 0);
+  else
+    store_codes8_tail(reinterpret_cast<int8_t*>(codes.at) + c, codes.cols - c, w);
+  if ((t & 3) == 0 && c < codes.cols) reinterpret_cast<uint8_t*>(scale.at)[c >> 5] = static_cast<uint8_t>(e);
 }
 // Parameters of either type.
 template <int TPR, bool kVec>
 __device__ __forceinline__ void fetch_param(const void* p, bool bf16, int cols, int t, int j, float (&v)[8]) {
   if (bf16)
-    fetch<uint16_t, TPR, kVec>(row_at(p, 0, cols * 2), t, j, v);
+    fetch<uint16_t, TPR, kVec>(row_at<uint16_t>(p, 0, cols), t, j, v);
   else
-    fetch<float, TPR, kVec>(row_at(p, 0, cols * 4), t, j, v);
+    fetch<float, TPR, kVec>(row_at<float>(p, 0, cols), t, j, v);
 }
 
 template <int TPR>
@@ -164,12 +160,12 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
   constexpr int kRows = kBlockThreads<TPR> / TPR;
   __shared__ float part[2 * TPR / 64];
   const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  const int cols = a.cols;
   const float count = static_cast<float>(cols);
   const int blocks = (cols + kAct8Block - 1) / kAct8Block;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
-    const Row x = row_at(a.x, row * row_bytes, row_bytes);
+    const Row x = row_at<T>(a.x, row, cols);
     float v[NC][8];
     float sum = 0.0f, none = 0.0f;
 #pragma unroll
@@ -185,7 +181,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[j][i] = column<TPR, kVec>(t, j, i) < cols ? v[j][i] - near : 0.0f;
+        v[j][i] = column<TPR>(t, j) + i < cols ? v[j][i] - near : 0.0f;
         off += v[j][i];
         sq = fmaf(v[j][i], v[j][i], sq);
       }
@@ -197,7 +193,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    const Row y = row_at(a.y, row * row_bytes, row_bytes);
+    const Row y = row_at<T>(a.y, row, cols);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       float o[8];
@@ -216,31 +212,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
       }
       put<T, TPR, kVec>(y, t, j, o);
       if (a.codes) {
-        const Row codes = row_at(a.codes, row * cols, cols), scale = row_at(a.scale, row * blocks, blocks);
-        if constexpr (kVec) {
-          const int c = column<TPR, true>(t, j, 0);
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m = max(m, act8_mag(v[j][i]));
-          const int e = static_cast<int>(quad_max(m) >> 23);
-          int q[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = act8_encode(v[j][i], e);
-          const u32x2 w = {act8_pack(q[0], q[1], q[2], q[3]), act8_pack(q[4], q[5], q[6], q[7])};
-          __builtin_amdgcn_raw_buffer_store_b64(w, codes.rsrc, c, 0, 0);
-          if ((t & 3) == 0)
-            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), scale.rsrc, scale.skip + (c >> 5), 0, 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = column<TPR, false>(t, j, i);
-            const int e = static_cast<int>(half_wave_max(act8_mag(v[j][i])) >> 23);
-            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(act8_encode(v[j][i], e)), codes.rsrc,
-                                                 codes.skip + c, 0, 0);
-            if ((t & 31) == 0)
-              __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), scale.rsrc, scale.skip + (c >> 5), 0, 0);
-          }
-        }
+        put_act8<TPR, kVec>(row_at<int8_t>(a.codes, row, cols), row_at<uint8_t>(a.scale, row, blocks), t, j, v[j]);
       }
     }
   }
@@ -258,33 +230,32 @@ __device__ __forceinline__ void fetch_xhat(const XhatRow& r, int t, int j, float
     fetch<T, TPR, kVec>(r.x, t, j, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (v[i] - r.mean) * r.rstd;
-  } else if constexpr (kVec) {
-    const int c = column<TPR, true>(t, j, 0);
-    const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r.x.rsrc, c, 0, 0);
-    const int e = __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, r.scale.skip + (c >> 5), 0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act8_decode(act8_byte(w[i >> 2], i & 3), e);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<TPR, false>(t, j, i);
-      const int8_t q = static_cast<int8_t>(__builtin_amdgcn_raw_buffer_load_b8(r.x.rsrc, r.x.skip + c, 0, 0));
-      v[i] = act8_decode(q, __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, r.scale.skip + (c >> 5), 0, 0));
+    const int c = column<TPR>(t, j);
+    uint2 w;
+    int e = 0;
+    if constexpr (kVec) {
+      const u32x2 q = __builtin_amdgcn_raw_buffer_load_b64(r.x.rsrc, c, 0, 0);
+      w = make_uint2(q[0], q[1]);
+      e = __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, c >> 5, 0, 0);
+    } else {
+      w = load_codes8_tail(reinterpret_cast<const int8_t*>(r.x.at) + c, r.x.cols - c);
+      if (c < r.x.cols) e = reinterpret_cast<const uint8_t*>(r.scale.at)[c >> 5];
     }
+    act8_decode8(w, e, v);
   }
 }
-
-__device__ __forceinline__ XhatRow xhat_row(const NormBwdLaunch& a, int64_t row, int row_bytes, bool act8) {
+template <typename T, bool kAct8>
+__device__ __forceinline__ XhatRow xhat_row(const NormBwdLaunch& a, int64_t row) {
   XhatRow r;
   r.rstd = a.rstd[row];
-  if (act8) {
-    const int blocks = (a.cols + kAct8Block - 1) / kAct8Block;
+  if constexpr (kAct8) {
     r.mean = 0.0f;
-    r.x = row_at(a.codes, row * a.cols, a.cols);
-    r.scale = row_at(a.scale, row * blocks, blocks);
+    r.x = row_at<int8_t>(a.codes, row, a.cols);
+    r.scale = row_at<uint8_t>(a.scale, row, (a.cols + kAct8Block - 1) / kAct8Block);
   } else {
     r.mean = a.mean[row];
-    r.x = row_at(a.x, row * row_bytes, row_bytes);
+    r.x = row_at<T>(a.x, row, a.cols);
   }
   return r;
 }
@@ -299,7 +270,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
   __shared__ float part[2 * TPR / 64];
   __shared__ float sums[kSums];  // [2][8 NC TPR], the rows of a workgroup joined one after the other
   const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  const int cols = a.cols;
   const float inv = 1.0f / static_cast<float>(cols);
   float dw[kHeld][8], db[kHeld][8], w[kHeld][8];
   auto weight = [&](int j, float (&v)[8]) {
@@ -315,8 +286,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
   }
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
-    const Row dy = row_at(a.dy, row * row_bytes, row_bytes);
-    const XhatRow xr = xhat_row(a, row, row_bytes, kAct8);
+    const Row dy = row_at<T>(a.dy, row, cols);
+    const XhatRow xr = xhat_row<T, kAct8>(a, row);
     float g[NC][8], xh[NC][8];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -331,7 +302,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
       if constexpr (!kParams) weight(j, w[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = column<TPR, kVec>(t, j, i) < cols;
+        const bool in = column<TPR>(t, j) + i < cols;
         const float d = g[j][i], x = in ? xh[j][i] : 0.0f;
         if constexpr (kParams) {
           dw[j][i] = fmaf(d, x, dw[j][i]);
@@ -348,7 +319,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
     s1 *= inv;
     s2 *= inv;
     if (a.dx) {
-      const Row dx = row_at(a.dx, row * row_bytes, row_bytes);
+      const Row dx = row_at<T>(a.dx, row, cols);
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         float o[8];
@@ -383,8 +354,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
           db[j][i] = sums[8 * NC * TPR + s];
         }
     }
-    float* ws = a.workspace + static_cast<int64_t>(blockIdx.x) * 2 * cols;
-    const Row wdw = row_at(ws, 0, cols * 4), wdb = row_at(ws + cols, 0, cols * 4);
+    const Row wdw = row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.x), cols);
+    const Row wdb = row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + 1, cols);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       put<float, TPR, kVec>(wdw, t, j, dw[j]);
@@ -399,40 +370,56 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
 template <typename T, bool kVec, bool kAct8>
 __global__ void __launch_bounds__(256) quest_norm_colsum_kernel(const NormBwdLaunch a) {
   const int t = threadIdx.x, j = blockIdx.x;
-  const int cols = a.cols, row_bytes = cols * static_cast<int>(sizeof(T));
+  const int cols = a.cols;
   float dw[8] = {}, db[8] = {};
 #pragma unroll 2
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     float g[8], xh[8];
-    fetch<T, 256, kVec>(row_at(a.dy, row * row_bytes, row_bytes), t, j, g);
-    fetch_xhat<T, 256, kVec, kAct8>(xhat_row(a, row, row_bytes, kAct8), t, j, xh);
+    fetch<T, 256, kVec>(row_at<T>(a.dy, row, cols), t, j, g);
+    fetch_xhat<T, 256, kVec, kAct8>(xhat_row<T, kAct8>(a, row), t, j, xh);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       dw[i] = fmaf(g[i], xh[i], dw[i]);
       db[i] += g[i];
     }
   }
-  float* ws = a.workspace + static_cast<int64_t>(blockIdx.y) * 2 * cols;
-  put<float, 256, kVec>(row_at(ws, 0, cols * 4), t, j, dw);
-  put<float, 256, kVec>(row_at(ws + cols, 0, cols * 4), t, j, db);
+  put<float, 256, kVec>(row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.y), cols), t, j, dw);
+  put<float, 256, kVec>(row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.y) + 1, cols), t, j, db);
 }
 
-// The workgroups' column sums added in a fixed order: thread (s, c) of a
-// workgroup adds every 4th of them from s for column c, then the four.
+// The workgroups' column sums added in a fixed order: slice s of a workgroup
+// adds every 16th of them from s for its 32 columns, 8 loads at a time, then
+// the slices are added.  Few columns a workgroup and many loads in flight:
+// the sums of 512 workgroups over 2048 columns take 4.2 us (31 us with 4 slices
+// of 64 columns and one load at a time, all of it latency).
+constexpr int kSlices = 16, kSumCols = 32;
 template <typename P>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSlices* kSumCols)
     quest_norm_params_kernel(const float* __restrict__ ws, int groups, int cols, P* __restrict__ dw,
                              P* __restrict__ db) {
-  __shared__ float part[4][64];
-  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;  // column of [dw | db]
+  __shared__ float part[kSlices][kSumCols];
+  const int lane = threadIdx.x % kSumCols, s = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + lane;  // column of [dw | db]
   float v = 0.0f;
-  if (c < 2 * cols)
-    for (int g = s; g < groups; g += 4) v += ws[static_cast<int64_t>(g) * 2 * cols + c];
+  if (c < 2 * cols) {
+    const float* p = ws + c;
+    const int64_t pitch = 2 * static_cast<int64_t>(cols);
+    int g = s;
+    for (; g + 7 * kSlices < groups; g += 8 * kSlices) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p[(g + i * kSlices) * pitch];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += x[i];
+    }
+    for (; g < groups; g += kSlices) v += p[g * pitch];
+  }
   part[s][lane] = v;
   __syncthreads();
   if (s != 0 || c >= 2 * cols) return;
-  v = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) v += part[i][lane];
   if (c < cols) {
     if (dw) dw[c] = from_f32<P>(v);
   } else if (db) {
@@ -512,8 +499,10 @@ hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16) {
 
 int norm_bwd_groups(int64_t rows, int64_t cols) {
   const int64_t per = cols <= 2048 ? 4 : 1;  // rows a workgroup holds at a time
-  const int64_t n = (rows + per - 1) / per;
-  return static_cast<int>(n < 512 ? n : 512);
+  // as many workgroups as fit the chip by their registers (more of them only
+  // write more sums)
+  const int64_t n = (rows + per - 1) / per, most = cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;
+  return static_cast<int>(n < most ? n : most);
 }
 
 hipError_t launch_norm_bwd(const NormBwdLaunch& a, bool bf16) {
@@ -525,12 +514,12 @@ hipError_t launch_norm_bwd(const NormBwdLaunch& a, bool bf16) {
     if (e != hipSuccess) return e;
   }
   if (a.dweight || a.dbias) {
-    const dim3 grid((2 * a.cols + 63) / 64);
+    const dim3 grid((2 * a.cols + kSumCols - 1) / kSumCols), block(kSlices * kSumCols);
     if (a.param_bf16)
-      hipLaunchKernelGGL(quest_norm_params_kernel<uint16_t>, grid, dim3(256), 0, a.stream, a.workspace, groups,
+      hipLaunchKernelGGL(quest_norm_params_kernel<uint16_t>, grid, block, 0, a.stream, a.workspace, groups,
                          a.cols, static_cast<uint16_t*>(a.dweight), static_cast<uint16_t*>(a.dbias));
     else
-      hipLaunchKernelGGL(quest_norm_params_kernel<float>, grid, dim3(256), 0, a.stream, a.workspace, groups, a.cols,
+      hipLaunchKernelGGL(quest_norm_params_kernel<float>, grid, block, 0, a.stream, a.workspace, groups, a.cols,
                          static_cast<float*>(a.dweight), static_cast<float*>(a.dbias));
     return hipGetLastError();
   }
