@@ -698,7 +698,7 @@ quest_status quest_gated_fwd(const uint8_t* x, const float* x_scale, int64_t n, 
   if (x_bits < 1 || x_bits > 4 || w_bits < 1 || w_bits > 4) return QUEST_EUNSUPPORTED;
   if (!dtype_ok(out_dtype) || !act_ok(act) || n < 0 || m < 0 || k <= 0) return QUEST_EINVAL;
   if (k % 128 != 0 || k > kGemmMaxK || m > kGemmMaxN || n > kGemmMaxM) return QUEST_EUNSUPPORTED;
-  // 512 work-items per tile: the launch's work-item count must fit 32 bits.
+  // 256 work-items per 128 x 128 tile: the launch's work-item count must fit 32 bits.
   if (((n + 255) / 256) * ((m + 127) / 128) > kGemmMaxTiles) return QUEST_EUNSUPPORTED;
   if (n == 0 || m == 0) return QUEST_OK;
   if (!x || !x_scale || !gate || !gate_scale || !up || !up_scale || !out) return QUEST_EINVAL;

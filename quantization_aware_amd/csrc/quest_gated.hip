@@ -10,12 +10,21 @@
 //   g[i][j] = acc[i][j] * ((sx[i] kx) * (sg[j] kw))
 // has three roundings and then the activation's.
 //
-// Kernel: a workgroup of 8 waves computes 256 rows x 128 columns of h.  The
-// two weight operands' 4 + 4 blocks of 32 columns stand side by side in a
-// stage of LDS, so that a wave of 64 rows x 64 columns holds its gate and up
-// accumulators (2 x 2 blocks of 32 columns by 2 blocks of 32 rows) in the same
-// lanes and registers: lane l has row l % 32 and 4 consecutive columns per
-// register quad of both.  Stages stream into LDS three deep, as in quest_gemm.
+// Kernel: a workgroup of 4 waves computes 64 kB rows x 64 kB columns of h.  The
+// two weight operands' blocks of 32 columns stand side by side in a stage of
+// LDS, so that a wave holds its gate and up accumulators (kB blocks of 32
+// columns by kB blocks of 32 rows each) in the same lanes and registers: lane l
+// has row l % 32 and 4 consecutive columns per register quad of both.
+// kB = 2: two workgroups share a compute unit, each with two stages of 36 KB;
+// one's waits, activations and stores run beside the other's products.
+// 16384 x 2048 -> 5632 takes 258 us (2.93 PFLOP/s), 296 us with both
+// checkpoints; the products alone 212.  Bound by power: the clock is at 1.7 of
+// 2.4 GHz, the matrix cores 38% and LDS 50% busy, and work taken away anywhere
+// shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking its
+// tiles, the next one's first stages requested before the stores: 252 and 306 us.)
+// kB = 1: four times the workgroups, for products whose larger tiles would
+// leave compute units without one; 256 rows take 10.6 us (15.8 with kB = 2), 512 15.4
+// (16.7), 1024 would take 27.1 (25.4).
 #include <type_traits>
 
 #include "quest_act8.h"
@@ -24,10 +33,6 @@
 
 namespace quest {
 namespace {
-
-constexpr int kRowsTile = 256, kColsTile = 128;  // workgroup tile of h
-constexpr int kXStage = 8 * kBlock;              // x's 256 rows of a stage
-constexpr int kStage = 2 * kXStage;              // and 4 + 4 blocks of gate and up
 
 // act(g) and act'(g).  kFast: the hardware's reciprocal and exp2 (about 2^-22
 // relative), for values that are rounded to bf16 next; fp32 results take the
@@ -69,169 +74,59 @@ __device__ __forceinline__ void store_chunk(T* dst, const uint8_t* src, int left
   }
 }
 
-template <typename Out, bool kVec, bool kAct8>
-__global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a) {
+template <typename Out, int kB>
+constexpr int kSlabPitch = 32 * kB * static_cast<int>(sizeof(Out)) + 16;  // bytes of a slab's row, 32 rows a slab
+
+// What a wave does with its sums of gate (acc[0 .. kB - 1]) and up (the others) of
+// rows row0 + row1 .. and columns wcol ..: its kB blocks of 32 rows, each through
+// the wave's slab of LDS, so that a row's 32 kB columns leave together.
+// fx_at, fg_at, fu_at: Delta's factors of those rows and columns.  The windows
+// start at row0 and hold `rows_left` rows.
+template <typename Out, int kB, bool kVec, bool kAct8, int kAct>
+__device__ __forceinline__ void gated_epilogue(const GatedLaunch& a, v16f (&acc)[2 * kB][kB], const float* fx_at,
+                                               const float* fg_at, const float* fu_at, uint8_t* slab, int row0,
+                                               int row1, int rows_left, int wcol, int lane) {
   constexpr int kOut = static_cast<int>(sizeof(Out));
-  constexpr int kPer = 16 / kOut;             // outputs per 16-byte chunk
-  constexpr int kLanesPerRow = 64 / kPer;     // a wave's 64 columns
-  constexpr int kPitch = 64 * kOut + 16;      // slab row pitch in bytes
-  constexpr int kPitch8 = 128 + 16;           // codes: 64 of gate, 64 of up
-  static_assert(8 * 32 * kPitch <= 2 * kStage && kPitch8 <= kPitch, "slabs fit the second and third stage buffers");
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage + (256 + 2 * 128) * 4];
-  auto stage_mem = [&](auto bi) -> uint8_t* { return lds + decltype(bi)::value * kStage; };
-  float* const fac = reinterpret_cast<float*>(lds + 3 * kStage);  // [256] x, [128] gate, [128] up clip scales
-
-  const int n = a.n, m = a.m, k = a.k;
-  const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
-  const int lane = tid & 63;
-  const int stages = k >> 7;
-  const uint32_t rb_bytes = static_cast<uint32_t>(stages) * kBlock;  // one 32-row block, all of k
-  const int tiles_m = (n + kRowsTile - 1) / kRowsTile, tiles_n = (m + kColsTile - 1) / kColsTile;
-  // Workgroups are dealt to the 8 XCDs round-robin; each XCD takes a
-  // contiguous range of tiles, whose operand blocks then share its L2.
-  int pid = blockIdx.x, tm, tn;
-  const int full = static_cast<int>(gridDim.x) & ~7;
-  if (pid < full) pid = (pid & 7) * (full >> 3) + (pid >> 3);
-  tile_at(pid, tiles_m, tiles_n, tm, tn);
-  const int row0 = tm * kRowsTile, col0 = tn * kColsTile;
-
-  const int rb_x = (n + 31) >> 5, rb_w = (m + 31) >> 5;
-  const i32x4 rx = raw_rsrc(a.x + static_cast<size_t>(tm) * 8 * rb_bytes, min(rb_x - tm * 8, 8) * rb_bytes);
-  const uint32_t w_bytes = min(rb_w - tn * 4, 4) * rb_bytes;
-  const i32x4 rg = raw_rsrc(a.gate + static_cast<size_t>(tn) * 4 * rb_bytes, w_bytes);
-  const i32x4 ru = raw_rsrc(a.up + static_cast<size_t>(tn) * 4 * rb_bytes, w_bytes);
-
-  // The clip scales: wave w < 4 rows 64 w ..., waves 4 and 5 gate's columns, 6 and 7 up's.
-  {
-    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(fac)) + 256 * wave;
-    const float* src = wave < 4 ? a.sx + row0 + 64 * wave : (wave < 6 ? a.sg : a.su) + col0 + 64 * (wave & 1);
-    const int left = wave < 4 ? n - row0 - 64 * wave : m - col0 - 64 * (wave & 1);
-    dma4(base, lane * 4, raw_rsrc(src, __builtin_amdgcn_readfirstlane(max(min(left, 64), 0)) * 4));
-  }
-
-  // Stage st into LDS: 24 wave instructions for x and 24 for the weights,
-  // wave w issuing w + 8 u, u < 3, of each.
-  constexpr int kLoads = 6;
-  auto fetch_stage = [&](int st, auto bi) {
-    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage_mem(bi)));
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int t = wave + 8 * u, blk = t / 3, part = t % 3;
-      const int off = st * kBlock + part * 1024 + lane * 16;
-      const uint32_t la = base + blk * kBlock + part * 1024;
-      dma16(__builtin_amdgcn_readfirstlane(la), blk * static_cast<int>(rb_bytes) + off, rx);
-      dma16(__builtin_amdgcn_readfirstlane(la + kXStage), (blk & 3) * static_cast<int>(rb_bytes) + off,
-            blk < 4 ? rg : ru);
-    }
-  };
-  // Fragment (block rbk of x (op 0) or of the weights (op 1), k-half ks): this lane's 24 bytes.
-  auto frag = [&](auto bi, int op, int rbk, int ks) -> v8i {
-    const u32x2* s =
-        reinterpret_cast<const u32x2*>(stage_mem(bi) + op * kXStage + rbk * kBlock + ks * kFrag + lane * 24);
-    const u32x2 x0 = s[0], x1 = s[1], x2 = s[2];
-    return v8i{static_cast<int>(x0[0]), static_cast<int>(x0[1]), static_cast<int>(x1[0]),
-               static_cast<int>(x1[1]), static_cast<int>(x2[0]), static_cast<int>(x2[1]), 0, 0};
-  };
-  // Weight block j of a wave: gate 2 wn, 2 wn + 1, then up's.
-  auto wblk = [&](int j) { return (j & 1) + 2 * wn + 4 * (j >> 1); };
-
-  fetch_stage(0, I0{});
-  fetch_stage(stages > 1 ? 1 : 0, I1{});
-  v16f acc[4][2];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) acc[j][i] = v16f{};
-  wait_vmcnt<kLoads>();
-  lds_barrier();
-  v8i f0x[2], f0w[4], f1x[2], f1w[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) f0x[i] = frag(I0{}, 0, wm * 2 + i, 0);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f0w[j] = frag(I0{}, 1, wblk(j), 0);
-  // One stage: bi holds stage s, bn stage s + 1, b2 receives stage s + 2 (it
-  // last held stage s - 1, whose reads every wave finished before the previous
-  // barrier).  Stages past the last are the last one again, so that every wait
-  // counts the same loads.
-  auto step = [&](int s, auto bi, auto bn, auto b2) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) f1x[i] = frag(bi, 0, wm * 2 + i, 1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f1w[j] = frag(bi, 1, wblk(j), 1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0w[j], f0x[i], acc[j][i], 2, 2, 0, 127, 0, 127);
-    fetch_stage(s + 2 < stages ? s + 2 : stages - 1, b2);
-    wait_vmcnt<kLoads>();
-    lds_barrier();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) f0x[i] = frag(bn, 0, wm * 2 + i, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f0w[j] = frag(bn, 1, wblk(j), 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1w[j], f1x[i], acc[j][i], 2, 2, 0, 127, 0, 127);
-  };
-  int s = 0;
-  for (; s + 3 <= stages; s += 3) {
-    step(s, I0{}, I1{}, I2{});
-    step(s + 1, I1{}, I2{}, I0{});
-    step(s + 2, I2{}, I0{}, I1{});
-  }
-  if (s < stages) step(s++, I0{}, I1{}, I2{});
-  if (s < stages) step(s++, I1{}, I2{}, I0{});
-  wait_vmcnt<0>();  // no load into LDS in flight before it is reused
-  lds_barrier();
-
-  // Epilogue: each wave goes through its two blocks of 32 rows, in a slab of
-  // LDS of its own.
-  uint8_t* slab = lds + kStage + wave * 32 * kPitch;
-  const int rows_left = min(n - row0, kRowsTile);
+  constexpr int kPer = 16 / kOut;               // outputs per 16-byte chunk
+  constexpr int kLanesPerRow = 32 * kB / kPer;  // a wave's columns
+  constexpr int kPitch = kSlabPitch<Out, kB>;
+  constexpr int kCodes = 32 * kB;  // a row's codes of gate, then up's
+  static_assert(2 * kCodes + 16 <= kPitch, "the codes fit the slab");
+  const int m = a.m;
   const auto rout = make_rsrc(static_cast<Out*>(a.out) + static_cast<size_t>(row0) * m,
                               static_cast<uint32_t>(rows_left) * static_cast<uint32_t>(m) * kOut);
   const int r32 = lane & 31, h = lane >> 5;
-  const int wcol = col0 + wn * 64;  // the wave's first column
   auto slab_fence = [&]() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float fx = fac[wm * 64 + 32 * i + r32] * a.kx;
-    uint32_t code[2][2][4];  // [gate, up][block][quad]
-    int ex[2][2];
+  for (int i = 0; i < kB; ++i) {
+    const float fx = fx_at[32 * i + r32];
+    uint32_t code[2][kB][4];  // [gate, up][block][quad]
+    int ex[2][kB];
 #pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-      uint32_t mg = 0, mu = 0;
+    for (int jj = 0; jj < kB; ++jj) {
+      // Columns past m have clip scale 0, so g = u = 0 there.
+      float mg = 0.0f, mu = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int cl = 32 * jj + 8 * q + 4 * h;  // column within the wave's 64
-        const float4 sg = *reinterpret_cast<const float4*>(&fac[256 + wn * 64 + cl]);
-        const float4 su = *reinterpret_cast<const float4*>(&fac[384 + wn * 64 + cl]);
+        const int cl = 32 * jj + 8 * q + 4 * h;  // column within the wave's
+        const float4 sg = *reinterpret_cast<const float4*>(&fg_at[cl]);
+        const float4 su = *reinterpret_cast<const float4*>(&fu_at[cl]);
         const float kg[4] = {sg.x, sg.y, sg.z, sg.w}, ku[4] = {su.x, su.y, su.z, su.w};
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float gv = acc[jj][i][4 * q + e] * (fx * (kg[e] * a.kw));
-          const float uv = acc[2 + jj][i][4 * q + e] * (fx * (ku[e] * a.kw));
-          y[e] = act_value<kOut == 2>(gv, a.act) * uv;
+          const float gv = acc[jj][i][4 * q + e] * (fx * kg[e]);
+          const float uv = acc[kB + jj][i][4 * q + e] * (fx * ku[e]);
+          y[e] = act_value<kOut == 2>(gv, kAct) * uv;
           if constexpr (kAct8) {
             acc[jj][i][4 * q + e] = gv;
-            acc[2 + jj][i][4 * q + e] = uv;
-            if (wcol + cl + e < m) {
-              mg = max(mg, act8_mag(gv));
-              mu = max(mu, act8_mag(uv));
-            }
+            acc[kB + jj][i][4 * q + e] = uv;
+            mg = fmaxf(mg, fabsf(gv));
+            mu = fmaxf(mu, fabsf(uv));
           }
         }
         uint8_t* d = slab + r32 * kPitch + cl * kOut;
@@ -244,24 +139,21 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
       }
       if constexpr (kAct8) {
         // the block's other 16 columns are in lane ^ 32
-        ex[0][jj] = static_cast<int>(halves_max(mg) >> 23);
-        ex[1][jj] = static_cast<int>(halves_max(mu) >> 23);
+        ex[0][jj] = static_cast<int>(halves_max(act8_mag(mg)) >> 23);
+        ex[1][jj] = static_cast<int>(halves_max(act8_mag(mu)) >> 23);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            int c[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = act8_encode(acc[2 * p + jj][i][4 * q + e], ex[p][jj]);
-            code[p][jj][q] = act8_pack(c[0], c[1], c[2], c[3]);
-          }
+          for (int q = 0; q < 4; ++q)
+            code[p][jj][q] = act8_encode4(acc[kB * p + jj][i][4 * q], acc[kB * p + jj][i][4 * q + 1],
+                                          acc[kB * p + jj][i][4 * q + 2], acc[kB * p + jj][i][4 * q + 3], ex[p][jj]);
       }
     }
     slab_fence();
 #pragma unroll
     for (int t = 0; t < 32 * kLanesPerRow / 64; ++t) {
       const int sr = t * (64 / kLanesPerRow) + lane / kLanesPerRow, sc = (lane % kLanesPerRow) * kPer;
-      const int row = wm * 64 + 32 * i + sr, col = wcol + sc;
+      const int row = row1 + 32 * i + sr, col = wcol + sc;
       const uint8_t* src = slab + sr * kPitch + sc * kOut;
       if constexpr (kVec) {
         const int off = col < m ? (row * m + col) * kOut : kNowhereOff;
@@ -276,10 +168,10 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
+        for (int jj = 0; jj < kB; ++jj)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint32_t*>(slab + r32 * kPitch8 + 64 * p + 32 * jj + 8 * q + 4 * h) = code[p][jj][q];
+            *reinterpret_cast<uint32_t*>(slab + r32 * kPitch + kCodes * p + 32 * jj + 8 * q + 4 * h) = code[p][jj][q];
       slab_fence();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -288,10 +180,10 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
         const auto re = make_rsrc((p ? a.up_scale : a.gate_scale) + static_cast<size_t>(row0) * blocks,
                                   static_cast<uint32_t>(rows_left) * static_cast<uint32_t>(blocks));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int sr = t * 16 + lane / 4, sc = (lane % 4) * 16;
-          const int row = wm * 64 + 32 * i + sr, col = wcol + sc;
-          const uint8_t* src = slab + sr * kPitch8 + 64 * p + sc;
+        for (int t = 0; t < kB; ++t) {
+          const int sr = t * (32 / kB) + lane / (2 * kB), sc = (lane % (2 * kB)) * 16;
+          const int row = row1 + 32 * i + sr, col = wcol + sc;
+          const uint8_t* src = slab + sr * kPitch + kCodes * p + sc;
           if constexpr (kVec) {
             const int off = col < m ? row * m + col : kNowhereOff;
             __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(src), rc, off, 0, 0);
@@ -300,16 +192,141 @@ __global__ void __launch_bounds__(512, 1) quest_gated_kernel(const GatedLaunch a
                                 m - col);
           }
         }
-        // the exponents of block h of the wave's two
-        const int blk = (wcol >> 5) + h;
-        const int e = h ? ex[p][1] : ex[p][0];
+        // the exponents: with two blocks, the lower lanes the first one's
+        const int blk = (wcol >> 5) + (kB == 2 ? h : 0);
+        const int e = kB == 2 && h ? ex[p][kB - 1] : ex[p][0];
         __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(e), re,
-                                             blk < blocks ? (wm * 64 + 32 * i + r32) * blocks + blk : kNowhereOff, 0,
-                                             0);
+                                             blk < blocks ? (row1 + 32 * i + r32) * blocks + blk : kNowhereOff, 0, 0);
       }
       slab_fence();
     }
   }
+}
+
+template <typename Out, int kB, bool kVec, bool kAct8, int kAct>
+__global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const GatedLaunch a) {
+  constexpr int kTile = 64 * kB;             // rows and columns of h of a workgroup
+  constexpr int kOpStage = 2 * kB * kBlock;  // one operand's blocks of a stage
+  constexpr int kStage = 3 * kOpStage;       // x, gate and up
+  constexpr int kSlab = 32 * kSlabPitch<Out, kB>;
+  static_assert(4 * kSlab <= 2 * kStage, "the waves' slabs fit the stage buffers");
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 3 * kTile * 4];
+  auto stage_mem = [&](auto bi) -> uint8_t* { return lds + decltype(bi)::value * kStage; };
+  float* const fac = reinterpret_cast<float*>(lds + 2 * kStage);  // clip scales: kTile each of x, gate and up
+
+  const int n = a.n, m = a.m, k = a.k;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int lane = tid & 63;
+  const int stages = k >> 7;
+  const uint32_t rb_bytes = static_cast<uint32_t>(stages) * kBlock;  // one 32-row block, all of k
+  const int tiles_m = (n + kTile - 1) / kTile, tiles_n = (m + kTile - 1) / kTile;
+  // Workgroups are dealt to the 8 XCDs round-robin; each XCD takes a
+  // contiguous range of tiles, whose operand blocks then share its L2.
+  int pid = blockIdx.x, tm, tn;
+  const int full = static_cast<int>(gridDim.x) & ~7;
+  if (pid < full) pid = (pid & 7) * (full >> 3) + (pid >> 3);
+  tile_at(pid, tiles_m, tiles_n, tm, tn);
+  const int row0 = tm * kTile, col0 = tn * kTile;
+
+  const int rb_x = (n + 31) >> 5, rb_w = (m + 31) >> 5;
+  const i32x4 rx = raw_rsrc(a.x + static_cast<size_t>(tm) * 2 * kB * rb_bytes, min(rb_x - tm * 2 * kB, 2 * kB) * rb_bytes);
+  const uint32_t w_bytes = min(rb_w - tn * 2 * kB, 2 * kB) * rb_bytes;
+  const i32x4 rg = raw_rsrc(a.gate + static_cast<size_t>(tn) * 2 * kB * rb_bytes, w_bytes);
+  const i32x4 ru = raw_rsrc(a.up + static_cast<size_t>(tn) * 2 * kB * rb_bytes, w_bytes);
+
+  // The clip scales, 64 a load (entries past the end as zeros): kB of each, in turn by the waves.
+  auto fetch_scales = [&](int op, const float* src, int left) {
+#pragma unroll
+    for (int v = 0; v < kB; ++v) {
+      if (((op * kB + v) & 3) != wave) continue;
+      const int first = 64 * v;
+      dma4(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(fac + op * kTile + first))), lane * 4,
+           raw_rsrc(src + first, __builtin_amdgcn_readfirstlane(max(min(left - first, 64), 0)) * 4));
+    }
+  };
+  fetch_scales(0, a.sx + row0, n - row0);
+  fetch_scales(1, a.sg + col0, m - col0);
+  fetch_scales(2, a.su + col0, m - col0);
+
+  // Stage st into LDS: 6 kB wave instructions for each operand, spread over the
+  // waves (for kB = 1, where they are one and a half a wave, from another wave on
+  // for each operand).
+  auto fetch_stage = [&](int st, auto bi) {
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage_mem(bi)));
+    auto fetch_operand = [&](int op, i32x4 rsrc) {
+#pragma unroll
+      for (int v = 0; v < (6 * kB + 3) / 4; ++v) {
+        const int t = ((wave + 2 * op) & 3) + 4 * v;
+        if (6 * kB % 4 == 0 || t < 6 * kB) {
+          const int blk = t / 3, part = t % 3;
+          const int off = blk * static_cast<int>(rb_bytes) + st * kBlock + part * 1024 + lane * 16;
+          dma16(__builtin_amdgcn_readfirstlane(base + op * kOpStage + blk * kBlock + part * 1024), off, rsrc);
+        }
+      }
+    };
+    fetch_operand(0, rx);
+    fetch_operand(1, rg);
+    fetch_operand(2, ru);
+  };
+  // Fragment (block rbk of x (op 0), gate (1) or up (2), k-half ks): this lane's 24 bytes.
+  auto frag = [&](auto bi, int op, int rbk, int ks) -> v8i {
+    const u32x2* s =
+        reinterpret_cast<const u32x2*>(stage_mem(bi) + op * kOpStage + rbk * kBlock + ks * kFrag + lane * 24);
+    const u32x2 x0 = s[0], x1 = s[1], x2 = s[2];
+    return v8i{static_cast<int>(x0[0]), static_cast<int>(x0[1]), static_cast<int>(x1[0]),
+               static_cast<int>(x1[1]), static_cast<int>(x2[0]), static_cast<int>(x2[1]), 0, 0};
+  };
+
+  fetch_stage(0, I0{});
+  v16f acc[2 * kB][kB];
+#pragma unroll
+  for (int j = 0; j < 2 * kB; ++j)
+#pragma unroll
+    for (int i = 0; i < kB; ++i) acc[j][i] = v16f{};
+  // One stage: bi holds it; the other buffer held the stage before, whose reads
+  // every wave finished before the barrier, and receives the next one.
+  auto step = [&](int s, auto bi, auto bn) {
+    wait_vmcnt<0>();  // this wave's part of stage s has landed (it had a stage's time)
+    lds_barrier();
+    if (s + 1 < stages) fetch_stage(s + 1, bn);
+    v8i fx[2][kB], fw[2][2 * kB];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < kB; ++i) fx[h][i] = frag(bi, 0, wm * kB + i, h);
+#pragma unroll
+      for (int j = 0; j < 2 * kB; ++j) fw[h][j] = frag(bi, 1 + j / kB, wn * kB + j % kB, h);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2 * kB; ++j)
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+          acc[j][i] =
+              __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[h][j], fx[h][i], acc[j][i], 2, 2, 0, 127, 0, 127);
+  };
+  // Delta's factors, once for all (between the first barrier and the last).
+  auto delta = [&]() {
+    for (int t = tid; t < 3 * kTile; t += 256) fac[t] *= t < kTile ? a.kx : a.kw;
+  };
+  int s = 0;
+  for (; s + 2 <= stages; s += 2) {
+    step(s, I0{}, I1{});
+    if (s == 0) delta();
+    step(s + 1, I1{}, I0{});
+  }
+  if (s < stages) step(s, I0{}, I1{});
+  if (stages == 1) delta();
+  lds_barrier();  // every wave's reads are done before the buffers are reused
+
+  gated_epilogue<Out, kB, kVec, kAct8, kAct>(a, acc, fac + wm * 32 * kB, fac + kTile + wn * 32 * kB,
+                                             fac + 2 * kTile + wn * 32 * kB, lds + wave * kSlab, row0, wm * 32 * kB,
+                                             min(n - row0, kTile), col0 + wn * 32 * kB, lane);
 }
 
 // Few rows (a decode step): the weights are the work, each read once, and a
@@ -439,7 +456,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) quest_gated_few_kernel(const G
 // Backward: 8 columns a thread, a row a workgroup at a time; rows that are no
 // whole 16 bytes at unaligned addresses, the last columns one by one.  A
 // streaming kernel: 8.06 bytes an entry in bf16.
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kAct>
 __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaunch a) {
   const int cols = a.cols, blocks = (cols + kAct8Block - 1) / kAct8Block;
   constexpr bool kFast = sizeof(T) == 2;
@@ -469,7 +486,7 @@ __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaun
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float value, slope;
-        act_both<kFast>(g[i], a.act, value, slope);
+        act_both<kFast>(g[i], kAct, value, slope);
         g[i] = d[i] * u[i] * slope;
         u[i] = d[i] * value;
       }
@@ -484,14 +501,25 @@ __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaun
   }
 }
 
-template <typename Out, bool kVec>
-hipError_t launch(const GatedLaunch& g) {
-  const int tiles = ((g.n + kRowsTile - 1) / kRowsTile) * ((g.m + kColsTile - 1) / kColsTile);
-  if (g.gate_codes)
-    hipLaunchKernelGGL((quest_gated_kernel<Out, kVec, true>), dim3(tiles), dim3(512), 0, g.stream, g);
+template <typename Out, int kB, bool kVec>
+hipError_t launch_tiles(const GatedLaunch& g) {
+  constexpr int kTile = 64 * kB;
+  const dim3 grid(((g.n + kTile - 1) / kTile) * ((g.m + kTile - 1) / kTile)), block(256);
+  if (g.gate_codes && g.act == 0)
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, true, 0>), grid, block, 0, g.stream, g);
+  else if (g.gate_codes)
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, true, 1>), grid, block, 0, g.stream, g);
+  else if (g.act == 0)
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, false, 0>), grid, block, 0, g.stream, g);
   else
-    hipLaunchKernelGGL((quest_gated_kernel<Out, kVec, false>), dim3(tiles), dim3(512), 0, g.stream, g);
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, false, 1>), grid, block, 0, g.stream, g);
   return hipGetLastError();
+}
+
+template <typename Out, bool kVec>
+hipError_t launch_tiles(const GatedLaunch& g) {
+  const int tiles = ((g.n + 127) / 128) * ((g.m + 127) / 128);
+  return tiles >= device_cus() ? launch_tiles<Out, 2, kVec>(g) : launch_tiles<Out, 1, kVec>(g);
 }
 
 template <typename Out, int kT>
@@ -510,16 +538,21 @@ hipError_t launch_fwd(const GatedLaunch& g) {
   if (g.n <= 32) return launch_few<Out, 2>(g);
   if (g.n <= 64) return launch_few<Out, 4>(g);
   // Rows whose chunks of 16 codes and of 16 bytes of output start on 16 bytes.
-  return g.m % 16 == 0 ? launch<Out, true>(g) : launch<Out, false>(g);
+  return g.m % 16 == 0 ? launch_tiles<Out, true>(g) : launch_tiles<Out, false>(g);
 }
 
 template <typename T>
 hipError_t launch_bwd(const GatedBwdLaunch& a) {
   const dim3 grid(static_cast<uint32_t>(a.rows < (1 << 20) ? a.rows : (1 << 20)));
-  if (a.cols % 8 == 0)
-    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, true>), grid, dim3(256), 0, a.stream, a);
+  const bool vec = a.cols % 8 == 0;
+  if (vec && a.act == 0)
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, true, 0>), grid, dim3(256), 0, a.stream, a);
+  else if (vec)
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, true, 1>), grid, dim3(256), 0, a.stream, a);
+  else if (a.act == 0)
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, false, 0>), grid, dim3(256), 0, a.stream, a);
   else
-    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, false>), grid, dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL((quest_gated_bwd_kernel<T, false, 1>), grid, dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
 
