@@ -233,3 +233,35 @@ def test_non_contiguous_tensors_are_refused(lib):
     for call in (lambda: qa.act8_save(t(40, 4).t()), lambda: qa.layer_norm_fwd(t(4, 80)[:, ::2])):
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------------------
+# The modules
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kw,exc", [
+    (dict(features=192, width=256), ValueError), (dict(features=256, width=256, block=96), ValueError),
+    (dict(features=256, width=200), ValueError), (dict(features=256, width=256, bits_x=5), ValueError),
+    (dict(features=256, width=256, bits_w=0), ValueError), (dict(features=256, width=256, act="relu"), ValueError),
+    (dict(features=256, width=256, compute_dtype=torch.float16), TypeError),
+])
+def test_block_rejects(kw, exc):
+    from quantization_aware_amd.feedforward import QuestFeedForward
+
+    with pytest.raises(exc):
+        QuestFeedForward(**kw)
+
+
+def test_modules_on_the_cpu_refuse(lib):
+    from quantization_aware_amd.feedforward import LayerNorm, QuestFeedForward, layer_norm, quest_gated
+
+    ff = QuestFeedForward(128, 256)
+    assert [n for n, _ in ff.named_parameters()] == ["gate", "up", "norm.weight", "norm.bias", "down.weight"]
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ff(t(3, 128))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        layer_norm(t(3, 128))
+    with pytest.raises(ValueError, match="the last axis of x has 100"):
+        LayerNorm(128)(t(3, 100))
+    with pytest.raises(ValueError, match="got"):
+        quest_gated(t(3, 128), t(8, 256), t(8, 256))
