@@ -660,15 +660,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without making a torch.cuda.Stream of it (a tenth of the time), where torch has that.
+# Small calls cost what the host does.  The current stream's handle and the current device's number come straight
+# from torch's C module where it has them (torch.cuda.current_stream makes a Stream object first, 1.9 us against 0.1).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_DTYPE_CODES = {torch.bfloat16: QUEST_BF16, torch.float32: QUEST_F32}
 
 
 def _launch(call: str, dev: torch.device, stream, *args) -> None:
     """One device call of the library on `stream` (default: dev's current stream), with dev the current device."""
-    fn = getattr(load_library(), call)
+    fn = getattr(_lib or load_library(), call)
     handle = _raw_stream(dev.index) if stream is None and _raw_stream else _stream_handle(dev, stream)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -677,10 +680,19 @@ def _launch(call: str, dev: torch.device, stream, *args) -> None:
         _check(call, status)
 
 
-def _matrix(name: str, t) -> None:
+def _matrix(name: str, t) -> int:
+    """The type's code of a 2-D float32 or bfloat16 tensor."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor (rows x cols)")
-    _dtype_code(t)
+    code = _DTYPE_CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def _float_code(dtype) -> int:
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"libquest takes float32 or bfloat16 tensors, got {dtype}")
+    return code
 
 
 def _exactly(name: str, t, dtype, shape) -> None:
@@ -694,17 +706,19 @@ def _exactly(name: str, t, dtype, shape) -> None:
 
 
 def _check_tensors(dev: torch.device, *specs) -> None:
-    """Every (name, tensor, dtype, shape) of that type and shape (a number: at least so many elements),
-    contiguous and on the GPU `dev`.  Types and sizes are checked before any device; the loop that finds
-    everything in order is kept short, since small calls cost what the host does."""
+    """Every (name, tensor, dtype, shape) of that type and shape (a number: at least so many elements; None:
+    any), contiguous and on the GPU `dev`.  The short loop finds everything in order; where it does not, types and
+    sizes are gone through before any device."""
+    index = dev.index
     for _, t, dtype, shape in specs:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_cuda
-                and t.is_contiguous() and (t.numel() >= shape if type(shape) is int else t.shape == shape)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and (shape is None or (t.numel() >= shape if type(shape) is int else t.shape == shape))):
             break
     else:
-        return
+        if dev.type == "cuda":
+            return
     for name, t, dtype, shape in specs:
-        (_buffer if type(shape) is int else _exactly)(name, t, dtype, shape)
+        (_buffer if type(shape) is int else _exactly)(name, t, dtype, t.shape if shape is None else shape)
     _on_device(dev, **{name: t for name, t, _, _ in specs})
 
 
@@ -727,15 +741,18 @@ def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
     codes: int8 (rows, cols); scale: uint8 (rows, ceil(cols / 32)), the biased
     power-of-two exponent of each block of 32 columns.  Allocated unless given.
     """
-    _matrix("x", x)
+    code = _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
-    if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    if scale is None:
-        scale = torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=dev)
-    _check_tensors(dev, ("x", x, x.dtype, x.shape), *_act8_specs("the checkpoint's", (codes, scale), rows, cols))
-    _launch("quest_act8_save", dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, codes.data_ptr(),
+    specs = (("x", x, x.dtype, None),)
+    if codes is None and scale is None:
+        codes, scale = _new_act8(rows, cols, dev)
+    else:
+        new = _new_act8(rows, cols, dev)
+        codes, scale = new[0] if codes is None else codes, new[1] if scale is None else scale
+        specs += _act8_specs("the checkpoint's", (codes, scale), rows, cols)
+    _check_tensors(dev, *specs)
+    _launch("quest_act8_save", dev, stream, x.data_ptr(), code, rows, cols, codes.data_ptr(),
             scale.data_ptr())
     return codes, scale
 
@@ -747,13 +764,15 @@ def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16
         raise ValueError("codes must be a 2-D tensor (rows x cols)")
     rows, cols = codes.shape
     dev = codes.device
+    specs = _act8_specs("the checkpoint's", (codes, scale), rows, cols)
     if out is None:
+        code = _float_code(out_dtype)
         out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    _matrix("out", out)
-    _check_tensors(dev, *_act8_specs("the checkpoint's", (codes, scale), rows, cols),
-                   ("out", out, out.dtype, (rows, cols)))
-    _launch("quest_act8_load", dev, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(),
-            _dtype_code(out))
+    else:
+        code = _matrix("out", out)
+        specs += (("out", out, out.dtype, (rows, cols)),)
+    _check_tensors(dev, *specs)
+    _launch("quest_act8_load", dev, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(), code)
     return out
 
 
@@ -767,7 +786,7 @@ def _norm_params(cols: int, weight, bias):
             raise TypeError(f"{name} must be a torch.Tensor")
         if specs and t.dtype != specs[0][2]:
             raise TypeError(f"weight and bias must share one type, got {weight.dtype} and {bias.dtype}")
-        code = _dtype_code(t)
+        code = _float_code(t.dtype)
         specs += ((name, t, t.dtype, (cols,)),)
     return specs, code
 
@@ -781,17 +800,20 @@ def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, a
     (rows,), and with act8 the (codes, scale) of the normalised input's 8-bit
     checkpoint for layer_norm_bwd (otherwise None).
     """
-    _matrix("x", x)
+    code = _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
-    params, param_code = _norm_params(cols, weight, bias)
+    specs, param_code = _norm_params(cols, weight, bias)
+    specs += (("x", x, x.dtype, None),)
+    if out is not None:
+        specs += (("out", out, x.dtype, x.shape),)
+    _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty_like(x)
-    _check_tensors(dev, ("x", x, x.dtype, x.shape), ("out", out, x.dtype, x.shape), *params)
     mean = torch.empty((rows,), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     codes, scale = _new_act8(rows, cols, dev) if act8 else (None, None)
-    _launch("quest_layer_norm_fwd", dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ptr(weight), _ptr(bias),
+    _launch("quest_layer_norm_fwd", dev, stream, x.data_ptr(), code, rows, cols, _ptr(weight), _ptr(bias),
             param_code, float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(codes), _ptr(scale))
     return out, mean, rstd, (codes, scale) if act8 else None
 
@@ -806,7 +828,7 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
     not asked for is None.  Parameter gradients have the weight's type, or
     param_dtype (default float32) without one.
     """
-    _matrix("dy", dy)
+    code = _matrix("dy", dy)
     rows, cols = dy.shape
     dev = dy.device
     if weight_grad is None:
@@ -825,7 +847,7 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
     param_dtype = weight.dtype if weight is not None else param_dtype or torch.float32
     if param_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"parameter gradients are float32 or bfloat16, not {param_dtype}")
-    _check_tensors(dev, ("dy", dy, dy.dtype, dy.shape), ("rstd", rstd, torch.float32, (rows,)), *source, *params)
+    _check_tensors(dev, ("dy", dy, dy.dtype, None), ("rstd", rstd, torch.float32, (rows,)), *source, *params)
     dx = torch.empty_like(dy) if input_grad else None
     dweight = torch.empty((cols,), dtype=param_dtype, device=dev) if weight_grad else None
     dbias = torch.empty((cols,), dtype=param_dtype, device=dev) if bias_grad else None
@@ -835,7 +857,7 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
         ws = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
         if stream is not None and stream != torch.cuda.current_stream(dev):
             ws.record_stream(stream)  # its memory is not handed out again before the call there has run
-    _launch("quest_layer_norm_bwd", dev, stream, dy.data_ptr(), _dtype_code(dy), rows, cols, _ptr(x), _ptr(mean),
+    _launch("quest_layer_norm_bwd", dev, stream, dy.data_ptr(), code, rows, cols, _ptr(x), _ptr(mean),
             _ptr(codes), _ptr(scale), rstd.data_ptr(), _ptr(weight),
             QUEST_BF16 if param_dtype == torch.bfloat16 else QUEST_F32, _ptr(dx), _ptr(dweight), _ptr(dbias),
             _ptr(ws))
@@ -859,23 +881,29 @@ def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate:
     products for gated_bwd (otherwise None).
     """
     n, m, k = int(n), int(m), int(k)
-    code = _act_code(act)
+    act_code = _act_code(act)
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     dev = x.device
+    # (sizes that the library refuses need no bytes here)
+    per_block = k * 24 if k > 0 and k % 128 == 0 else 0  # of 32 operand rows
+    nx, nw = (max(n, 0) + 31) // 32 * per_block, (max(m, 0) + 31) // 32 * per_block
+    specs = (("x", x, torch.uint8, nx), ("x_scale", x_scale, torch.float32, n), ("gate", gate, torch.uint8, nw),
+             ("gate_scale", gate_scale, torch.float32, m), ("up", up, torch.uint8, nw),
+             ("up_scale", up_scale, torch.float32, m))
+    if out is None:
+        code = _float_code(out_dtype)
+    else:
+        code = _matrix("out", out)
+        specs += (("out", out, out.dtype, (n, m)),)
+    _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty((n, m), dtype=out_dtype, device=dev)
-    _matrix("out", out)
-    nx, nw = operand_bytes(n, k), operand_bytes(m, k)
-    _check_tensors(dev, ("x", x, torch.uint8, nx), ("x_scale", x_scale, torch.float32, n),
-                   ("gate", gate, torch.uint8, nw), ("gate_scale", gate_scale, torch.float32, m),
-                   ("up", up, torch.uint8, nw), ("up_scale", up_scale, torch.float32, m),
-                   ("out", out, out.dtype, (n, m)))
     gate8 = _new_act8(n, m, dev) if act8 else (None, None)
     up8 = _new_act8(n, m, dev) if act8 else (None, None)
     _launch("quest_gated_fwd", dev, stream, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
-            gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(), m, int(w_bits), k, code, out.data_ptr(),
-            _dtype_code(out), _ptr(gate8[0]), _ptr(gate8[1]), _ptr(up8[0]), _ptr(up8[1]))
+            gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(), m, int(w_bits), k, act_code, out.data_ptr(),
+            code, _ptr(gate8[0]), _ptr(gate8[1]), _ptr(up8[0]), _ptr(up8[1]))
     return (out, gate8, up8) if act8 else (out, None, None)
 
 
@@ -885,14 +913,16 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
     Returns (rows, 2 cols) of dh's type: the gradient reaching the gate product
     in the first cols columns, the one reaching the up product in the others.
     """
-    _matrix("dh", dh)
+    code = _matrix("dh", dh)
     rows, cols = dh.shape
     dev = dh.device
-    code = _act_code(act)
+    act_code = _act_code(act)
+    specs = (("dh", dh, dh.dtype, None), *_act8_specs("gate8", gate8, rows, cols), *_act8_specs("up8", up8, rows, cols))
+    if out is not None:
+        specs += (("out", out, dh.dtype, (rows, 2 * cols)),)
+    _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dev)
-    _check_tensors(dev, ("dh", dh, dh.dtype, dh.shape), *_act8_specs("gate8", gate8, rows, cols),
-                   *_act8_specs("up8", up8, rows, cols), ("out", out, dh.dtype, (rows, 2 * cols)))
-    _launch("quest_gated_bwd", dev, stream, dh.data_ptr(), _dtype_code(dh), rows, cols, gate8[0].data_ptr(),
-            gate8[1].data_ptr(), up8[0].data_ptr(), up8[1].data_ptr(), code, out.data_ptr())
+    _launch("quest_gated_bwd", dev, stream, dh.data_ptr(), code, rows, cols, gate8[0].data_ptr(), gate8[1].data_ptr(),
+            up8[0].data_ptr(), up8[1].data_ptr(), act_code, out.data_ptr())
     return out
