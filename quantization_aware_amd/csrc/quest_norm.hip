@@ -164,6 +164,22 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
   const float count = static_cast<float>(cols);
   const int blocks = (cols + kAct8Block - 1) / kAct8Block;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  // The parameters in registers across the rows that a workgroup walks (16384 x
+  // 2048 bf16 with fp32 parameters: 27.4 us, 31.9 when every row reads them again
+  // from the caches); not beside the entries of the widest rows, whose threads
+  // have 128 registers.
+  constexpr bool kHold = TPR * NC < 4096;
+  float w[kHold ? NC : 1][8], b[kHold ? NC : 1][8];
+  auto params = [&](int j, float (&wj)[8], float (&bj)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wj[i] = 1.0f, bj[i] = 0.0f;
+    if (a.weight) fetch_param<TPR, kVec>(a.weight, a.param_bf16, cols, t, j, wj);
+    if (a.bias) fetch_param<TPR, kVec>(a.bias, a.param_bf16, cols, t, j, bj);
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) params(j, w[j], b[j]);
+  }
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
     const Row x = row_at<T>(a.x, row, cols);
     float v[NC][8];
@@ -196,19 +212,13 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
     const Row y = row_at<T>(a.y, row, cols);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      const int held = kHold ? j : 0;
+      if constexpr (!kHold) params(j, w[0], b[0]);
       float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = v[j][i] = (v[j][i] - off) * rstd;
-      float p[8];
-      if (a.weight) {
-        fetch_param<TPR, kVec>(a.weight, a.param_bf16, cols, t, j, p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= p[i];
-      }
-      if (a.bias) {
-        fetch_param<TPR, kVec>(a.bias, a.param_bf16, cols, t, j, p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += p[i];
+      for (int i = 0; i < 8; ++i) {
+        v[j][i] = (v[j][i] - off) * rstd;
+        o[i] = fmaf(v[j][i], w[held][i], b[held][i]);
       }
       put<T, TPR, kVec>(y, t, j, o);
       if (a.codes) {
@@ -427,7 +437,10 @@ __global__ void __launch_bounds__(kSlices* kSumCols)
   }
 }
 
-constexpr int kMaxFwdBlocks = 1 << 20;  // more rows are walked
+// Workgroups of the forward and of dx alone, which walk the rows beyond.  The
+// stores of y are ordinary ones: non-temporal they make the norm alone faster
+// (23.1 us), but not with the quantiser that reads y next (49.0 us both, 47.6 so).
+constexpr int kMaxFwdBlocks = 2048;
 constexpr int kMaxHeldCols = 16384;      // widest rows whose backward holds entries and column sums in registers
 
 template <typename T, int TPR, int NC, bool kVec>
