@@ -441,6 +441,12 @@ __global__ void __launch_bounds__(kSlices* kSumCols)
 // stores of y are ordinary ones: non-temporal they make the norm alone faster
 // (23.1 us), but not with the quantiser that reads y next (49.0 us both, 47.6 so).
 constexpr int kMaxFwdBlocks = 2048;
+// Up to so many rows of 513 to 2048 columns (a row for each of the backward's
+// workgroups) a row has a workgroup's 256 threads and not a wave's 64, whose chain
+// of loads and sums is what such a call takes: 1 x 2048 forward 2.4 us against 3.8,
+// backward 2.4 against 5.4; 256 x 2048 3.4 against 5.0 and 5.1 against 6.9; at 1000
+// rows the backward of 1024 columns would take 7.5 against 5.4.
+constexpr int kFewRows = 512;
 constexpr int kMaxHeldCols = 16384;      // widest rows whose backward holds entries and column sums in registers
 
 template <typename T, int TPR, int NC, bool kVec>
@@ -456,6 +462,7 @@ hipError_t fwd(const NormFwdLaunch& a) {
 template <typename T, bool kVec>
 hipError_t fwd_width(const NormFwdLaunch& a) {
   if (a.cols <= 512) return fwd<T, 64, 1, kVec>(a);
+  if (a.rows <= kFewRows && a.cols <= 2048) return fwd<T, 256, 1, kVec>(a);
   if (a.cols <= 1024) return fwd<T, 64, 2, kVec>(a);
   if (a.cols <= 2048) return fwd<T, 64, 4, kVec>(a);
   if (a.cols <= 4096) return fwd<T, 256, 2, kVec>(a);
@@ -487,6 +494,7 @@ hipError_t bwd_width(const NormBwdLaunch& a, int groups) {
     if (e != hipSuccess || !a.dx) return e;
   } else if (a.workspace) {
     if (a.cols <= 512) return bwd<T, 64, 1, kVec, true>(a, groups);
+    if (a.rows <= kFewRows && a.cols <= 2048) return bwd<T, 256, 1, kVec, true>(a, groups);
     if (a.cols <= 1024) return bwd<T, 64, 2, kVec, true>(a, groups);
     if (a.cols <= 2048) return bwd<T, 64, 4, kVec, true>(a, groups);
     if (a.cols <= 4096) return bwd<T, 256, 2, kVec, true>(a, groups);
@@ -511,7 +519,7 @@ hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16) {
 }
 
 int norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 2048 ? 4 : 1;  // rows a workgroup holds at a time
+  const int64_t per = cols <= 512 || (cols <= 2048 && rows > kFewRows) ? 4 : 1;  // rows a workgroup holds at a time
   // as many workgroups as fit the chip by their registers (more of them only
   // write more sums)
   const int64_t n = (rows + per - 1) / per, most = cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;

@@ -10,6 +10,7 @@ import math
 
 import numpy as np
 import torch
+from scipy.special import erfc
 
 U = 2.0 ** -24
 BLOCK = 32
@@ -138,9 +139,6 @@ def check(name: str, got: torch.Tensor, want: np.ndarray, err: np.ndarray) -> fl
 # The gated product
 # ---------------------------------------------------------------------------
 
-_erfc = np.vectorize(math.erfc, otypes=[np.float64])
-
-
 def act(g, name):
     """act(g), act'(g) and bounds of their fp32 errors for an exact g (about 2 ulp per function call, the
     exponent's and erfc's arguments rounded: relative 2 |g| U and 2 g^2 U)."""
@@ -149,7 +147,7 @@ def act(g, name):
         c = 1.0 / (1.0 + np.exp(g))
         rel = (2 * np.abs(g) + 10) * U
         return g * s, s + g * s * c, np.abs(g) * s * rel, (s + np.abs(g) * s * (c + 2 * U / np.maximum(rel, U))) * rel
-    phi = 0.5 * _erfc(-g / math.sqrt(2.0))
+    phi = 0.5 * erfc(-g / math.sqrt(2.0))
     dens = np.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
     rel = (2 * g * g + 20) * U
     return g * phi, phi + g * dens, np.abs(g) * phi * rel, (phi + np.abs(g) * dens) * rel

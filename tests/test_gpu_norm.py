@@ -25,7 +25,7 @@ def dev():
 
 SHAPES = [(1, 1), (5, 2), (1, 2048), (3, 7), (64, 31), (9, 32), (130, 100), (2050, 64), (33, 512), (40, 513), (7, 1000),
           (65, 1111), (18, 2048), (6, 2056), (5, 2049), (9, 4096), (4, 5632), (3, 8192), (3, 8200), (2, 9001),
-          (3, 16384), (2, 16392), (5, 20001), (3, 32768), (600, 96)]
+          (3, 16384), (2, 16392), (5, 20001), (3, 32768), (600, 96), (515, 1000), (1030, 640), (520, 2048), (513, 1111)]
 
 
 def inputs(rows, cols, dtype, pdtype, seed, offset=0.3):
