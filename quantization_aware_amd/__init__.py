@@ -667,10 +667,19 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _DTYPE_CODES = {torch.bfloat16: QUEST_BF16, torch.float32: QUEST_F32}
 
 
-def _launch(call: str, dev: torch.device, stream, *args) -> None:
-    """One device call of the library on `stream` (default: dev's current stream), with dev the current device."""
+def _on_stream(stream, *tensors):
+    """`stream` as the current one, for a call on it: outputs and workspaces are then its own memory, which is
+    neither still in use on another stream nor handed out again before the call has run."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(call: str, dev: torch.device, *args) -> None:
+    """One device call of the library on dev's current stream, with dev the current device."""
     fn = getattr(_lib or load_library(), call)
-    handle = _raw_stream(dev.index) if stream is None and _raw_stream else _stream_handle(dev, stream)
+    handle = _raw_stream(dev.index) if _raw_stream else _stream_handle(dev, None)
     if _current_device() == dev.index:
         status = fn(*args, handle)
     else:
@@ -741,6 +750,9 @@ def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
     codes: int8 (rows, cols); scale: uint8 (rows, ceil(cols / 32)), the biased
     power-of-two exponent of each block of 32 columns.  Allocated unless given.
     """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return act8_save(x, codes, scale)
     code = _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
@@ -752,7 +764,7 @@ def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
         codes, scale = new[0] if codes is None else codes, new[1] if scale is None else scale
         specs += _act8_specs("the checkpoint's", (codes, scale), rows, cols)
     _check_tensors(dev, *specs)
-    _launch("quest_act8_save", dev, stream, x.data_ptr(), code, rows, cols, codes.data_ptr(),
+    _launch("quest_act8_save", dev, x.data_ptr(), code, rows, cols, codes.data_ptr(),
             scale.data_ptr())
     return codes, scale
 
@@ -760,6 +772,9 @@ def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
 def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16, out=None,
               stream=None) -> torch.Tensor:
     """The values of an 8-bit checkpoint (quest_act8_load), exact in bfloat16 and float32."""
+    if stream is not None:
+        with _on_stream(stream, codes):
+            return act8_load(codes, scale, out_dtype, out)
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError("codes must be a 2-D tensor (rows x cols)")
     rows, cols = codes.shape
@@ -772,7 +787,7 @@ def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16
         code = _matrix("out", out)
         specs += (("out", out, out.dtype, (rows, cols)),)
     _check_tensors(dev, *specs)
-    _launch("quest_act8_load", dev, stream, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(), code)
+    _launch("quest_act8_load", dev, codes.data_ptr(), scale.data_ptr(), rows, cols, out.data_ptr(), code)
     return out
 
 
@@ -800,6 +815,9 @@ def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, a
     (rows,), and with act8 the (codes, scale) of the normalised input's 8-bit
     checkpoint for layer_norm_bwd (otherwise None).
     """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return layer_norm_fwd(x, weight, bias, eps, act8, out)
     code = _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
@@ -813,7 +831,7 @@ def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, a
     mean = torch.empty((rows,), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     codes, scale = _new_act8(rows, cols, dev) if act8 else (None, None)
-    _launch("quest_layer_norm_fwd", dev, stream, x.data_ptr(), code, rows, cols, _ptr(weight), _ptr(bias),
+    _launch("quest_layer_norm_fwd", dev, x.data_ptr(), code, rows, cols, _ptr(weight), _ptr(bias),
             param_code, float(eps), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(codes), _ptr(scale))
     return out, mean, rstd, (codes, scale) if act8 else None
 
@@ -828,6 +846,10 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
     not asked for is None.  Parameter gradients have the weight's type, or
     param_dtype (default float32) without one.
     """
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return layer_norm_bwd(dy, rstd, weight, x=x, mean=mean, act8=act8, input_grad=input_grad,
+                                  weight_grad=weight_grad, bias_grad=bias_grad, param_dtype=param_dtype)
     code = _matrix("dy", dy)
     rows, cols = dy.shape
     dev = dy.device
@@ -855,9 +877,7 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
     if weight_grad or bias_grad:
         need = int(load_library().quest_layer_norm_workspace_bytes(rows, cols))
         ws = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            ws.record_stream(stream)  # its memory is not handed out again before the call there has run
-    _launch("quest_layer_norm_bwd", dev, stream, dy.data_ptr(), code, rows, cols, _ptr(x), _ptr(mean),
+    _launch("quest_layer_norm_bwd", dev, dy.data_ptr(), code, rows, cols, _ptr(x), _ptr(mean),
             _ptr(codes), _ptr(scale), rstd.data_ptr(), _ptr(weight),
             QUEST_BF16 if param_dtype == torch.bfloat16 else QUEST_F32, _ptr(dx), _ptr(dweight), _ptr(dbias),
             _ptr(ws))
@@ -880,6 +900,10 @@ def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate:
     (n, m) of out_dtype and, with act8, the (codes, scale) checkpoints of both
     products for gated_bwd (otherwise None).
     """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return gated_fwd(x, x_scale, n, x_bits, gate, gate_scale, up, up_scale, m, w_bits, k, act, out_dtype, act8,
+                             out)
     n, m, k = int(n), int(m), int(k)
     act_code = _act_code(act)
     if not isinstance(x, torch.Tensor):
@@ -901,7 +925,7 @@ def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate:
         out = torch.empty((n, m), dtype=out_dtype, device=dev)
     gate8 = _new_act8(n, m, dev) if act8 else (None, None)
     up8 = _new_act8(n, m, dev) if act8 else (None, None)
-    _launch("quest_gated_fwd", dev, stream, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
+    _launch("quest_gated_fwd", dev, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
             gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(), m, int(w_bits), k, act_code, out.data_ptr(),
             code, _ptr(gate8[0]), _ptr(gate8[1]), _ptr(up8[0]), _ptr(up8[1]))
     return (out, gate8, up8) if act8 else (out, None, None)
@@ -913,6 +937,9 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
     Returns (rows, 2 cols) of dh's type: the gradient reaching the gate product
     in the first cols columns, the one reaching the up product in the others.
     """
+    if stream is not None:
+        with _on_stream(stream, dh):
+            return gated_bwd(dh, gate8, up8, act, out)
     code = _matrix("dh", dh)
     rows, cols = dh.shape
     dev = dh.device
@@ -923,6 +950,6 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
     _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dev)
-    _launch("quest_gated_bwd", dev, stream, dh.data_ptr(), code, rows, cols, gate8[0].data_ptr(), gate8[1].data_ptr(),
+    _launch("quest_gated_bwd", dev, dh.data_ptr(), code, rows, cols, gate8[0].data_ptr(), gate8[1].data_ptr(),
             up8[0].data_ptr(), up8[1].data_ptr(), act_code, out.data_ptr())
     return out

@@ -36,12 +36,16 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
     return t.clone() if t.data_ptr() % 16 else t
 
 
+def _differentiates(*tensors) -> bool:
+    """Whether a backward pass can follow (inside a Function's forward, torch.is_grad_enabled() no longer tells)."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class LayerNormFunction(torch.autograd.Function):
     """Layer norm of the rows of a 2-D x; see layer_norm."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps, act8):
-        act8 = act8 and any(ctx.needs_input_grad)
         y, mean, rstd, kept = layer_norm_fwd(x, weight, bias, eps, act8=act8)
         ctx.act8 = act8
         ctx.bias_dtype = None if bias is None else bias.dtype
@@ -68,7 +72,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     """
     flat = _dense(x.reshape(-1, x.shape[-1]))
     weight, bias = (None if t is None else _dense(t) for t in (weight, bias))
-    return LayerNormFunction.apply(flat, weight, bias, eps, act8).reshape(x.shape)
+    return LayerNormFunction.apply(flat, weight, bias, eps, act8 and _differentiates(flat, weight, bias)).reshape(x.shape)
 
 
 class LayerNorm(torch.nn.Module):
@@ -128,8 +132,7 @@ class QuestGatedFunction(torch.autograd.Function):
     """h = act(Q(x) Q(gate)^T) * (Q(x) Q(up)^T) for 2-D x; see quest_gated."""
 
     @staticmethod
-    def forward(ctx, x, gate, up, block, bits_x, bits_w, compute_dtype, act, trust_x, trust_w):
-        keep = any(ctx.needs_input_grad)
+    def forward(ctx, x, gate, up, block, bits_x, bits_w, compute_dtype, act, trust_x, trust_w, keep):
         ops, saved = _quantise_operands(x, gate, up, block, bits_x, bits_w, trust_x, trust_w, keep)
         (xo, xs), (go, gs), (uo, us) = ops
         (n, k), m = x.shape, gate.shape[0]
@@ -164,7 +167,7 @@ class QuestGatedFunction(torch.autograd.Function):
                 dequantize(wc[m:], ws[-m:], m, k, bits_w, out=qw[m:])
             g = torch.mm(dgu, qw)  # gradient reaching Q(x)
             dx = trust_bwd(g, xm, block, out=g).to(ctx.dtypes[0])
-        return dx, dg, du, None, None, None, None, None, None, None
+        return dx, dg, du, None, None, None, None, None, None, None, None
 
 
 def _check_gated(in_features: int, block: int, bits_x: int, bits_w: int, act: str, compute_dtype) -> None:
@@ -194,8 +197,9 @@ def quest_gated(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, block: in
     trust_x = default_trust(bits_x) if trust_x is None else trust_x
     trust_w = default_trust(bits_w) if trust_w is None else trust_w
     flat = _dense(x.reshape(-1, x.shape[-1]))
-    h = QuestGatedFunction.apply(flat, _dense(gate), _dense(up), block, bits_x, bits_w, compute_dtype, act, trust_x,
-                                 trust_w)
+    gate, up = _dense(gate), _dense(up)
+    h = QuestGatedFunction.apply(flat, gate, up, block, bits_x, bits_w, compute_dtype, act, trust_x, trust_w,
+                                 _differentiates(flat, gate, up))
     return h.reshape(*x.shape[:-1], gate.shape[0])
 
 

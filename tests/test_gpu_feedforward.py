@@ -193,6 +193,45 @@ def test_gated_without_gradient_and_empty(dev):
     assert h.shape == (0, 3, 72) and not gate.grad.any()
 
 
+def test_no_checkpoint_without_a_gradient(dev):
+    """Under no_grad nothing is kept, whatever the parameters require."""
+    log("no_grad allocates no checkpoint")
+    x, gate, up = (rand(s, i, torch.bfloat16, dev).requires_grad_() for i, s in
+                   enumerate(((4096, 128), (8192, 128), (8192, 128))))
+    quest_gated(x[:1], gate, up)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with torch.no_grad():
+        h = quest_gated(x, gate, up)
+    # h, the three operands and scales; the checkpoints would be two more bytes an entry of h
+    assert torch.cuda.max_memory_allocated() - before < 1.5 * h.numel() * 2
+
+
+def test_calls_on_their_own_stream(dev):
+    """A call given a stream takes its memory there: blocks that the current stream is still writing are not
+    among its outputs or its workspace."""
+    log("memory of a call on another stream")
+    rows, cols = 4096, 2048
+    x, dy = rand((rows, cols), 1, torch.bfloat16, dev), rand((rows, cols), 2, torch.bfloat16, dev)
+    w = rand((cols,), 3, torch.float32, dev)
+    y, mean, rstd, kept = qa.layer_norm_fwd(x, w, w, act8=True)
+    want = qa.layer_norm_bwd(dy, rstd, w, act8=kept, bias_grad=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        # freed blocks of the sizes the call needs, which the current stream writes for a while yet
+        junk = [torch.empty_like(x) for _ in range(2)] + [torch.empty(512 * 2 * cols, device=dev)]
+        for _ in range(20):
+            for j in junk:
+                j.fill_(7.0)
+        del junk
+        got = qa.layer_norm_bwd(dy, rstd, w, act8=kept, bias_grad=True, stream=side)
+        torch.cuda.synchronize()
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+
+
 def test_gated_refusals(dev):
     log("refusals")
     x, w = rand((4, 256), 1, torch.bfloat16, dev), rand((8, 256), 2, torch.bfloat16, dev)

@@ -178,3 +178,33 @@ def test_other_stream(dev):
     got_b = qa.gated_bwd(dh, got[1], got[2], stream=side)
     side.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want_b, got_b)
+
+
+def test_large_offsets(dev):
+    """More than 2^31 outputs (2^32 bytes of them): the last rows as a call on those rows alone gives them."""
+    n, k, m = (1 << 31) // 8192 + 96, 128, 8192
+    log(f"{n}x{k}x{m}")
+    x = torch.randn((n, k), device=dev).to(torch.bfloat16)
+    _, xs, _, xo = qa.quantize_fwd_op(x, 128, 4)
+    _, ts, _, to = qa.quantize_fwd_op(x[-96:].contiguous(), 128, 4)
+    w = [qa.quantize_fwd_op(torch.randn((m, k), device=dev).to(torch.bfloat16), 128, 4) for _ in range(2)]
+    args = (w[0][3], w[0][1], w[1][3], w[1][1], m, 4, k)
+    h, g8, u8 = qa.gated_fwd(xo, xs, n, 4, *args, act8=True)
+    th, tg, tu = qa.gated_fwd(to, ts, 96, 4, *args, act8=True)
+    assert torch.equal(h[-96:], th)
+    for a, c in zip((*g8, *u8), (*tg, *tu)):
+        assert torch.equal(a[-96:], c)
+    out = qa.gated_bwd(h, g8, u8)
+    assert torch.equal(out[-96:], qa.gated_bwd(th, tg, tu))
+
+
+def test_largest_k(dev):
+    """k = 32768 columns, the widest row the quantiser writes: the sums stay exact."""
+    n, k, m = 70, 32768, 64
+    log(f"{n}x{k}x{m}")
+    ops = case(dev, n, k, m, 4, 4)
+    for rows in (n, 20):
+        (xo, xs, lx) = quantised(dev, rows, k, 4, 1)
+        want, _, _, err, _, _ = fo.gated_fwd(lx, ops[1][2], ops[2][2], "silu")
+        h, _, _ = call(((xo, xs, lx), ops[1], ops[2]), rows, k, m, 4, 4, out_dtype=torch.float32)
+        fo.check("h", h, want, err)

@@ -218,3 +218,31 @@ def test_other_stream(dev):
     del junk
     for a, c in zip((*want[:3], *want_g), (*got[:3], *got_g)):
         assert torch.equal(a, c)
+
+
+def test_large_offsets(dev):
+    """More than 2^31 entries (2^32 bytes): the last rows, and the columns' sums of a gradient that is zero before them."""
+    rows, cols = (1 << 31) // 2048 + 64, 2048
+    log(f"{rows}x{cols}")
+    x = torch.randn((rows, cols), device=dev).to(torch.bfloat16)
+    w = torch.randn((cols,), device=dev)
+    y, mean, rstd, kept = qa.layer_norm_fwd(x, w, w, EPS, act8=True)
+    tail = x[-64:].contiguous()
+    ty, tmean, trstd, tkept = qa.layer_norm_fwd(tail, w, w, EPS, act8=True)
+    # (rows of a large call are a wave's, of a small one a workgroup's: the sums' orders differ)
+    assert torch.allclose(y[-64:].float(), ty.float(), rtol=2 ** -7, atol=1e-5)
+    assert torch.allclose(rstd[-64:], trstd, rtol=2e-6, atol=0)
+    check_fwd((y[-64:], mean[-64:], rstd[-64:], tuple(t[-64:] for t in kept)), tail, w, w)
+    dy = torch.zeros_like(x)
+    dy[-64:] = torch.randn((64, cols), device=dev).to(torch.bfloat16)
+    for src in (dict(act8=kept), dict(x=x, mean=mean)):
+        got = qa.layer_norm_bwd(dy, rstd, w, bias_grad=True, **src)
+        assert not got[0][:-64].any()
+        if "x" in src:
+            xhat = (fo.f64(tail) - fo.f64(mean[-64:])[:, None]) * fo.f64(rstd[-64:])[:, None]
+        else:
+            xhat = fo.act8_values(*(t[-64:].cpu().numpy() for t in kept))
+        args = (fo.f64(dy[-64:]), xhat, fo.f64(rstd[-64:]), fo.f64(w))
+        for name, g, want, err in zip(("dx", "dw", "db"), (got[0][-64:], *got[1:]), fo.norm_bwd(*args),
+                                      fo.norm_bwd_bounds(*args)):
+            fo.check(name, g, want, err)
