@@ -40,10 +40,23 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Sum over the 16 lanes of a row of the wave, in each of them.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp_or_zero<0xB1, 0xF>(v);
+  v += dpp_or_zero<0x4E, 0xF>(v);
+  v += dpp_or_zero<0x141, 0xF>(v);
+  return v + dpp_or_zero<0x140, 0xF>(v);
+}
+
 // Sums of two values over the TPR threads of a row; `part` holds 2 * TPR / 64
 // floats and is free again after the next call's first barrier.
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* part) {
+  if constexpr (TPR == 16) {
+    a = row16_sum(a);
+    b = row16_sum(b);
+    return;
+  }
   a = wave_sum(a);
   b = wave_sum(b);
   if constexpr (TPR > 64) {
@@ -153,13 +166,22 @@ __device__ __forceinline__ void fetch_param(const void* p, bool bf16, int cols, 
 }
 
 template <int TPR>
-constexpr int kBlockThreads = TPR == 64 ? 256 : TPR;
+constexpr int kBlockThreads = TPR <= 64 ? 256 : TPR;
+
+// Which of a workgroup's rows the thread is at: uniform over a wave, except where rows
+// have 16 threads (narrow ones, which go by address: kVec is false for them).
+template <int TPR>
+__device__ __forceinline__ int sub_row() {
+  const int sub = threadIdx.x / TPR;
+  return TPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub;
+}
 
 template <typename T, int TPR, int NC, bool kVec>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(const NormFwdLaunch a) {
   constexpr int kRows = kBlockThreads<TPR> / TPR;
-  __shared__ float part[2 * TPR / 64];
-  const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  __shared__ float part[TPR > 64 ? 2 * TPR / 64 : 1];
+  static_assert(TPR >= 64 || !kVec, "a wave's rows share a buffer resource");
+  const int t = threadIdx.x % TPR, sub = sub_row<TPR>();
   const int cols = a.cols;
   const float count = static_cast<float>(cols);
   const int blocks = (cols + kAct8Block - 1) / kAct8Block;
@@ -275,14 +297,19 @@ __device__ __forceinline__ XhatRow xhat_row(const NormBwdLaunch& a, int64_t row)
 template <typename T, int TPR, int NC, bool kVec, bool kAct8, bool kParams>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(const NormBwdLaunch a) {
   constexpr int kRows = kBlockThreads<TPR> / TPR;
-  constexpr int kSums = kParams && kRows > 1 ? 2 * 8 * NC * TPR : 1;
-  constexpr int kHeld = kParams ? NC : 1;
-  __shared__ float part[2 * TPR / 64];
+  // Rows of 1024 threads, which have 128 registers each: the sums of dy xhat in LDS,
+  // each thread's its own, and the weight read again from the caches for every row
+  // (2048 x 16384 bf16: 54.8 us, 67.2 with 512 threads and all in registers).
+  constexpr bool kWide = kParams && TPR == 1024;
+  constexpr int kSums = kWide ? 8 * NC * TPR : kParams && kRows > 1 ? 2 * 8 * NC * TPR : 1;
+  constexpr int kHeld = kParams ? NC : 1, kHeldW = kParams && !kWide ? NC : 1;
+  __shared__ float part[TPR > 64 ? 2 * TPR / 64 : 1];
   __shared__ float sums[kSums];  // [2][8 NC TPR], the rows of a workgroup joined one after the other
-  const int t = threadIdx.x % TPR, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  static_assert(TPR >= 64 || !kVec, "a wave's rows share a buffer resource");
+  const int t = threadIdx.x % TPR, sub = sub_row<TPR>();
   const int cols = a.cols;
   const float inv = 1.0f / static_cast<float>(cols);
-  float dw[kHeld][8], db[kHeld][8], w[kHeld][8];
+  float dw[kWide ? 1 : kHeld][8], db[kHeld][8], w[kHeldW][8];
   auto weight = [&](int j, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 1.0f;
@@ -291,8 +318,14 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j][i] = db[j][i] = 0.0f;
-    if constexpr (kParams) weight(j, w[j]);
+    for (int i = 0; i < 8; ++i) {
+      db[j][i] = 0.0f;
+      if constexpr (kWide)
+        sums[(8 * j + i) * TPR + t] = 0.0f;
+      else
+        dw[j][i] = 0.0f;
+    }
+    if constexpr (kParams && !kWide) weight(j, w[j]);
   }
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < a.rows; row += stride) {
@@ -308,14 +341,17 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int held = kParams ? j : 0;
-      if constexpr (!kParams) weight(j, w[0]);
+      const int held = kHeldW > 1 ? j : 0;
+      if constexpr (!kParams || kWide) weight(j, w[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = column<TPR>(t, j) + i < cols;
         const float d = g[j][i], x = in ? xh[j][i] : 0.0f;
         if constexpr (kParams) {
-          dw[j][i] = fmaf(d, x, dw[j][i]);
+          if constexpr (kWide)
+            sums[(8 * j + i) * TPR + t] += d * x;
+          else
+            dw[j][i] = fmaf(d, x, dw[j][i]);
           db[j][i] += d;
         }
         const float y = d * w[held][i];
@@ -368,7 +404,15 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
     const Row wdb = row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.x) + 1, cols);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      put<float, TPR, kVec>(wdw, t, j, dw[j]);
+      float sw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (kWide)
+          sw[i] = sums[(8 * j + i) * TPR + t];
+        else
+          sw[i] = dw[j][i];
+      }
+      put<float, TPR, kVec>(wdw, t, j, sw);
       put<float, TPR, kVec>(wdb, t, j, db[j]);
     }
   }
@@ -447,7 +491,12 @@ constexpr int kMaxFwdBlocks = 2048;
 // backward 2.4 against 5.4; 256 x 2048 3.4 against 5.0 and 5.1 against 6.9; at 1000
 // rows the backward of 1024 columns would take 7.5 against 5.4.
 constexpr int kFewRows = 512;
-constexpr int kMaxHeldCols = 16384;      // widest rows whose backward holds entries and column sums in registers
+// Rows of 16 threads: 111661 x 19 forward 13.5 us, 49.5 with a wave a row; backward 23.7
+// and 49.2.
+constexpr int kNarrowCols = 128;
+// Widest rows whose backward holds entries and column sums (1024 x 32768 bf16: 89 us
+// with the sums in a kernel of their own, 133 in one that spills).
+constexpr int kMaxHeldCols = 16384;
 
 template <typename T, int TPR, int NC, bool kVec>
 hipError_t fwd(const NormFwdLaunch& a) {
@@ -461,6 +510,7 @@ hipError_t fwd(const NormFwdLaunch& a) {
 
 template <typename T, bool kVec>
 hipError_t fwd_width(const NormFwdLaunch& a) {
+  if (a.cols <= kNarrowCols) return fwd<T, 16, 1, false>(a);
   if (a.cols <= 512) return fwd<T, 64, 1, kVec>(a);
   if (a.rows <= kFewRows && a.cols <= 2048) return fwd<T, 256, 1, kVec>(a);
   if (a.cols <= 1024) return fwd<T, 64, 2, kVec>(a);
@@ -493,17 +543,19 @@ hipError_t bwd_width(const NormBwdLaunch& a, int groups) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dx) return e;
   } else if (a.workspace) {
+    if (a.cols <= kNarrowCols) return bwd<T, 16, 1, false, true>(a, groups);
     if (a.cols <= 512) return bwd<T, 64, 1, kVec, true>(a, groups);
     if (a.rows <= kFewRows && a.cols <= 2048) return bwd<T, 256, 1, kVec, true>(a, groups);
     if (a.cols <= 1024) return bwd<T, 64, 2, kVec, true>(a, groups);
     if (a.cols <= 2048) return bwd<T, 64, 4, kVec, true>(a, groups);
     if (a.cols <= 4096) return bwd<T, 256, 2, kVec, true>(a, groups);
     if (a.cols <= 8192) return bwd<T, 256, 4, kVec, true>(a, groups);
-    return bwd<T, 512, 4, kVec, true>(a, groups);
+    return bwd<T, 1024, 2, kVec, true>(a, groups);
   }
   // dx alone: rows in workgroups of their own, as the forward
-  const int64_t n = a.cols <= 2048 ? (a.rows + 3) / 4 : a.rows;
+  const int64_t per = a.cols <= kNarrowCols ? 16 : a.cols <= 2048 ? 4 : 1, n = (a.rows + per - 1) / per;
   groups = static_cast<int>(n < kMaxFwdBlocks ? n : kMaxFwdBlocks);
+  if (a.cols <= kNarrowCols) return bwd<T, 16, 1, false, false>(a, groups);
   if (a.cols <= 512) return bwd<T, 64, 1, kVec, false>(a, groups);
   if (a.cols <= 2048) return bwd<T, 64, 4, kVec, false>(a, groups);
   if (a.cols <= 8192) return bwd<T, 256, 4, kVec, false>(a, groups);
@@ -519,10 +571,11 @@ hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16) {
 }
 
 int norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 512 || (cols <= 2048 && rows > kFewRows) ? 4 : 1;  // rows a workgroup holds at a time
-  // as many workgroups as fit the chip by their registers (more of them only
-  // write more sums)
-  const int64_t n = (rows + per - 1) / per, most = cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;
+  // rows a workgroup holds at a time
+  const int64_t per = cols <= kNarrowCols ? 16 : cols <= 512 || (cols <= 2048 && rows > kFewRows) ? 4 : 1;
+  // as many workgroups as fit the chip by their registers, or as their sums are
+  // soon added
+  const int64_t n = (rows + per - 1) / per, most = cols <= kNarrowCols ? 1024 : cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;
   return static_cast<int>(n < most ? n : most);
 }
 
