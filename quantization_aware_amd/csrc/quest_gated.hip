@@ -23,8 +23,7 @@
 // shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking its
 // tiles, the next one's first stages requested before the stores: 252 and 306 us.)
 // kB = 1: four times the workgroups, for products whose larger tiles would
-// leave compute units without one; 256 rows take 10.6 us (15.8 with kB = 2), 512 15.4
-// (16.7), 1024 would take 27.1 (25.4).
+// leave compute units without one; 256 rows take 10.5 us (15.4 with kB = 2).
 #include <type_traits>
 
 #include "quest_act8.h"
@@ -226,25 +225,30 @@ __device__ __forceinline__ void gated_epilogue(const GatedLaunch& a, v16f (&acc)
   }
 }
 
-template <typename Out, int kB, bool kVec, bool kAct8, int kAct>
-__global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const GatedLaunch a) {
+// kS: groups of 4 waves that share the tile, group g taking every kS-th stage from g,
+// in stage buffers of its own; their exact sums are added at the end.
+template <typename Out, int kB, int kS, bool kVec, bool kAct8, int kAct>
+__global__ void __launch_bounds__(256 * kS, 4 / kB) quest_gated_tiles_kernel(const GatedLaunch a) {
   constexpr int kTile = 64 * kB;             // rows and columns of h of a workgroup
   constexpr int kOpStage = 2 * kB * kBlock;  // one operand's blocks of a stage
   constexpr int kStage = 3 * kOpStage;       // x, gate and up
   constexpr int kSlab = 32 * kSlabPitch<Out, kB>;
   static_assert(4 * kSlab <= 2 * kStage, "the waves' slabs fit the stage buffers");
+  static_assert(kS == 1 || kB == 1, "a group's sums fit its stage buffers");
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 3 * kTile * 4];
-  auto stage_mem = [&](auto bi) -> uint8_t* { return lds + decltype(bi)::value * kStage; };
-  float* const fac = reinterpret_cast<float*>(lds + 2 * kStage);  // clip scales: kTile each of x, gate and up
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kS * kStage + 3 * kTile * 4];
+  float* const fac = reinterpret_cast<float*>(lds + 2 * kS * kStage);  // clip scales: kTile each of x, gate and up
 
   const int n = a.n, m = a.m, k = a.k;
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
+  const int group = kS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid) >> 8;
+  const int wave = (__builtin_amdgcn_readfirstlane(tid) >> 6) & 3;  // of the group
   const int wm = wave >> 1, wn = wave & 1;
   const int lane = tid & 63;
-  const int stages = k >> 7;
+  uint8_t* const own = lds + group * 2 * kStage;  // the group's buffers
+  auto stage_mem = [&](auto bi) -> uint8_t* { return own + decltype(bi)::value * kStage; };
+  const int stages = k >> 7, steps = (stages + kS - 1) / kS;
   const uint32_t rb_bytes = static_cast<uint32_t>(stages) * kBlock;  // one 32-row block, all of k
   const int tiles_m = (n + kTile - 1) / kTile, tiles_n = (m + kTile - 1) / kTile;
   // Workgroups are dealt to the 8 XCDs round-robin; each XCD takes a
@@ -271,14 +275,18 @@ __global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const Ga
            raw_rsrc(src + first, __builtin_amdgcn_readfirstlane(max(min(left - first, 64), 0)) * 4));
     }
   };
-  fetch_scales(0, a.sx + row0, n - row0);
-  fetch_scales(1, a.sg + col0, m - col0);
-  fetch_scales(2, a.su + col0, m - col0);
+  if (group == 0) {
+    fetch_scales(0, a.sx + row0, n - row0);
+    fetch_scales(1, a.sg + col0, m - col0);
+    fetch_scales(2, a.su + col0, m - col0);
+  }
 
   // Stage st into LDS: 6 kB wave instructions for each operand, spread over the
   // waves (for kB = 1, where they are one and a half a wave, from another wave on
-  // for each operand).
-  auto fetch_stage = [&](int st, auto bi) {
+  // for each operand).  A stage past the last, which some groups' last step has,
+  // lies outside the windows and is zeros.
+  auto fetch_stage = [&](int step, auto bi) {
+    const int st = step * kS + group;
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage_mem(bi)));
     auto fetch_operand = [&](int op, i32x4 rsrc) {
 #pragma unroll
@@ -286,7 +294,8 @@ __global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const Ga
         const int t = ((wave + 2 * op) & 3) + 4 * v;
         if (6 * kB % 4 == 0 || t < 6 * kB) {
           const int blk = t / 3, part = t % 3;
-          const int off = blk * static_cast<int>(rb_bytes) + st * kBlock + part * 1024 + lane * 16;
+          const int at = blk * static_cast<int>(rb_bytes) + st * kBlock + part * 1024 + lane * 16;
+          const int off = kS == 1 || st < stages ? at : kNowhereOff;
           dma16(__builtin_amdgcn_readfirstlane(base + op * kOpStage + blk * kBlock + part * 1024), off, rsrc);
         }
       }
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const Ga
   auto step = [&](int s, auto bi, auto bn) {
     wait_vmcnt<0>();  // this wave's part of stage s has landed (it had a stage's time)
     lds_barrier();
-    if (s + 1 < stages) fetch_stage(s + 1, bn);
+    if (s + 1 < steps) fetch_stage(s + 1, bn);
     v8i fx[2][kB], fw[2][2 * kB];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -335,17 +344,47 @@ __global__ void __launch_bounds__(256, 4 / kB) quest_gated_tiles_kernel(const Ga
   };
   // Delta's factors, once for all (between the first barrier and the last).
   auto delta = [&]() {
-    for (int t = tid; t < 3 * kTile; t += 256) fac[t] *= t < kTile ? a.kx : a.kw;
+    for (int t = tid; t < 3 * kTile; t += 256 * kS) fac[t] *= t < kTile ? a.kx : a.kw;
   };
   int s = 0;
-  for (; s + 2 <= stages; s += 2) {
+  for (; s + 2 <= steps; s += 2) {
     step(s, I0{}, I1{});
     if (s == 0) delta();
     step(s + 1, I1{}, I0{});
   }
-  if (s < stages) step(s, I0{}, I1{});
-  if (stages == 1) delta();
+  if (s < steps) step(s, I0{}, I1{});
+  if (steps == 1) delta();
   lds_barrier();  // every wave's reads are done before the buffers are reused
+  if constexpr (kS > 1) {
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    v4f* const sums = reinterpret_cast<v4f*>(lds) + (tid & 255);  // [group][2 kB * kB * 4][256]
+    constexpr int kQuads = 2 * kB * kB * 4;
+    static_assert(kQuads * 256 * 16 <= 2 * kStage, "a group's sums fit its stage buffers");
+    if (group > 0) {
+#pragma unroll
+      for (int j = 0; j < 2 * kB; ++j)
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sums[(group * kQuads + (j * kB + i) * 4 + q) * 256] =
+                v4f{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    }
+    lds_barrier();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < kS; ++g)
+#pragma unroll
+      for (int j = 0; j < 2 * kB; ++j)
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v4f v = sums[(g * kQuads + (j * kB + i) * 4 + q) * 256];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][i][4 * q + e] += v[e];
+          }
+  }
 
   gated_epilogue<Out, kB, kVec, kAct8, kAct>(a, acc, fac + wm * 32 * kB, fac + kTile + wn * 32 * kB,
                                              fac + 2 * kTile + wn * 32 * kB, lds + wave * kSlab, row0, wm * 32 * kB,
@@ -524,25 +563,32 @@ __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaun
   }
 }
 
-template <typename Out, int kB, bool kVec>
+template <typename Out, int kB, int kS, bool kVec>
 hipError_t launch_tiles(const GatedLaunch& g) {
   constexpr int kTile = 64 * kB;
-  const dim3 grid(((g.n + kTile - 1) / kTile) * ((g.m + kTile - 1) / kTile)), block(256);
+  const dim3 grid(((g.n + kTile - 1) / kTile) * ((g.m + kTile - 1) / kTile)), block(256 * kS);
   if (g.gate_codes && g.act == 0)
-    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, true, 0>), grid, block, 0, g.stream, g);
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kS, kVec, true, 0>), grid, block, 0, g.stream, g);
   else if (g.gate_codes)
-    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, true, 1>), grid, block, 0, g.stream, g);
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kS, kVec, true, 1>), grid, block, 0, g.stream, g);
   else if (g.act == 0)
-    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, false, 0>), grid, block, 0, g.stream, g);
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kS, kVec, false, 0>), grid, block, 0, g.stream, g);
   else
-    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kVec, false, 1>), grid, block, 0, g.stream, g);
+    hipLaunchKernelGGL((quest_gated_tiles_kernel<Out, kB, kS, kVec, false, 1>), grid, block, 0, g.stream, g);
   return hipGetLastError();
 }
 
 template <typename Out, bool kVec>
 hipError_t launch_tiles(const GatedLaunch& g) {
-  const int tiles = ((g.n + 127) / 128) * ((g.m + 127) / 128);
-  return tiles >= device_cus() ? launch_tiles<Out, 2, kVec>(g) : launch_tiles<Out, 1, kVec>(g);
+  const int cus = device_cus();
+  const int large = ((g.n + 127) / 128) * ((g.m + 127) / 128), small = ((g.n + 63) / 64) * ((g.m + 63) / 64);
+  // 64 x 64 tiles until the larger ones are a round and a quarter (2048 -> 5632, us): 512
+  // rows, 176 larger tiles, 14.4 against 16.1; 700, 264, 19.2 and 21.0; 1024, 352, 27.1 and 25.4.
+  if (4 * large >= 5 * cus) return launch_tiles<Out, 2, 1, kVec>(g);
+  // Long sums in few tiles are shared by four groups of waves: 357 x 7424 -> 1792 18.6
+  // against 27.5, 1365 x 8064 -> 256 19.4 and 29.3, but 128 x 2048 -> 5632 8.2 and 8.0.
+  if (small <= cus && g.k >= 4096) return launch_tiles<Out, 1, 4, kVec>(g);
+  return launch_tiles<Out, 1, 1, kVec>(g);
 }
 
 template <typename Out, int kT>

@@ -43,7 +43,7 @@ def call(ops, n, k, m, xb, wb, **kw):
 SHAPES = [(1, 128, 1, 4, 4), (1, 2048, 5632, 4, 4), (3, 256, 40, 2, 3), (17, 128, 33, 1, 1), (32, 640, 1001, 3, 2),
           (33, 384, 128, 4, 4), (48, 2048, 512, 4, 4), (64, 1024, 96, 4, 2), (65, 512, 260, 4, 4), (100, 896, 144, 2, 4),
           (128, 256, 1000, 4, 4), (129, 1152, 72, 4, 4), (255, 128, 130, 3, 3), (300, 640, 1001, 3, 2),
-          (513, 768, 400, 4, 4), (1030, 256, 264, 4, 1), (2050, 384, 2112, 4, 4), (2049, 128, 2101, 4, 3)]
+          (513, 768, 400, 4, 4), (1030, 256, 264, 4, 1), (2050, 384, 2112, 4, 4), (2049, 128, 2101, 4, 3), (130, 4224, 200, 4, 4), (70, 4480, 333, 3, 4)]
 
 
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
