@@ -18,9 +18,9 @@
 // kB = 2: two workgroups share a compute unit, each with two stages of 36 KB;
 // one's waits, activations and stores run beside the other's products.
 // 16384 x 2048 -> 5632 takes 258 us (2.93 PFLOP/s), 296 us with both
-// checkpoints; the products alone 212.  Bound by power: the clock is at 1.7 of
-// 2.4 GHz, the matrix cores 38% and LDS 50% busy, and work taken away anywhere
-// shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking its
+// checkpoints; the products alone 212.  Bound by power: the clock is at 1.7 to
+// 1.9 of 2.4 GHz, the matrix cores 38% and LDS 50% busy, and work taken away
+// anywhere shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking its
 // tiles, the next one's first stages requested before the stores: 252 and 306 us.)
 // kB = 1: four times the workgroups, for products whose larger tiles would
 // leave compute units without one; 256 rows take 10.5 us (15.4 with kB = 2).
