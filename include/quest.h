@@ -68,11 +68,16 @@ typedef enum {
   QUEST_STATUS_INT_RANGE_ = 0x7FFFFFFF /* not a status: gives the type int's range of values */
 } quest_status;
 
-/* Element types.  The last enumerator is not a type: it gives quest_dtype the
-   whole range of int, so that any value a caller passes can be received and
+/* Element types.  The last two enumerators are no types: they give quest_dtype
+   the whole range of int, so that any value a caller passes can be received and
    rejected with QUEST_EINVAL (in C++ a value outside an enumeration's range
    could not even be loaded). */
-typedef enum { QUEST_F32 = 0, QUEST_BF16 = 1, QUEST_DTYPE_INT_RANGE_ = 0x7FFFFFFF } quest_dtype;
+typedef enum {
+  QUEST_F32 = 0,
+  QUEST_BF16 = 1,
+  QUEST_DTYPE_INT_RANGE_ = 0x7FFFFFFF,
+  QUEST_DTYPE_INT_MIN_ = -0x7FFFFFFF - 1
+} quest_dtype;
 
 /* Largest row width handled in one pass (a row is reduced by one workgroup). */
 #define QUEST_MAX_COLS 32768
@@ -496,9 +501,8 @@ quest_status quest_act8_load(const int8_t* codes, const uint8_t* scale, int64_t 
  *   codes, scale  the 8-bit checkpoint of xhat (rounded from fp32) for
  *                 quest_layer_norm_bwd, or both NULL
  * 1 <= cols <= QUEST_MAX_COLS; rows, alignment and overlaps as for
- * quest_act8_save.  Infinities and NaN
- * stay within their row; a row's sum of squares about its mean must be finite
- * in fp32.
+ * quest_act8_save.  Infinities and NaN stay within their row; a row's sum, and
+ * its sum of squares about its mean, must be finite in fp32.
  */
 quest_status quest_layer_norm_fwd(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, const void* weight,
                                   const void* bias, quest_dtype param_dtype, double eps, void* y, float* mean,
@@ -531,7 +535,12 @@ quest_status quest_layer_norm_bwd(const void* dy, quest_dtype dtype, int64_t row
 
 /* Activations of the gated product: g / (1 + exp(-g)), and g * Phi(g) with the
    standard normal distribution function Phi. */
-typedef enum { QUEST_SILU = 0, QUEST_GELU = 1, QUEST_ACT_INT_RANGE_ = 0x7FFFFFFF } quest_act;
+typedef enum {
+  QUEST_SILU = 0,
+  QUEST_GELU = 1,
+  QUEST_ACT_INT_RANGE_ = 0x7FFFFFFF, /* these two: the range of int, as in quest_dtype */
+  QUEST_ACT_INT_MIN_ = -0x7FFFFFFF - 1
+} quest_act;
 
 /*
  * Gated product of quantised operands:

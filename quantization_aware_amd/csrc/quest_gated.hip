@@ -20,8 +20,9 @@
 // 16384 x 2048 -> 5632 takes 258 us (2.93 PFLOP/s), 296 us with both
 // checkpoints; the products alone 212.  Bound by power: the clock is at 1.7 to
 // 1.9 of 2.4 GHz, the matrix cores 38% and LDS 50% busy, and work taken away
-// anywhere shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking its
-// tiles, the next one's first stages requested before the stores: 252 and 306 us.)
+// anywhere shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking
+// its tiles, the next one's first stages requested before the stores: 252 and
+// 306 us.)
 // kB = 1: four times the workgroups, for products whose larger tiles would
 // leave compute units without one; 256 rows take 10.5 us (15.4 with kB = 2).
 #include <type_traits>
@@ -260,7 +261,8 @@ __global__ void __launch_bounds__(256 * kS, 4 / kB) quest_gated_tiles_kernel(con
   const int row0 = tm * kTile, col0 = tn * kTile;
 
   const int rb_x = (n + 31) >> 5, rb_w = (m + 31) >> 5;
-  const i32x4 rx = raw_rsrc(a.x + static_cast<size_t>(tm) * 2 * kB * rb_bytes, min(rb_x - tm * 2 * kB, 2 * kB) * rb_bytes);
+  const i32x4 rx =
+      raw_rsrc(a.x + static_cast<size_t>(tm) * 2 * kB * rb_bytes, min(rb_x - tm * 2 * kB, 2 * kB) * rb_bytes);
   const uint32_t w_bytes = min(rb_w - tn * 2 * kB, 2 * kB) * rb_bytes;
   const i32x4 rg = raw_rsrc(a.gate + static_cast<size_t>(tn) * 2 * kB * rb_bytes, w_bytes);
   const i32x4 ru = raw_rsrc(a.up + static_cast<size_t>(tn) * 2 * kB * rb_bytes, w_bytes);
@@ -271,7 +273,8 @@ __global__ void __launch_bounds__(256 * kS, 4 / kB) quest_gated_tiles_kernel(con
     for (int v = 0; v < kB; ++v) {
       if (((op * kB + v) & 3) != wave) continue;
       const int first = 64 * v;
-      dma4(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(fac + op * kTile + first))), lane * 4,
+      const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(fac + op * kTile + first));
+      dma4(__builtin_amdgcn_readfirstlane(to), lane * 4,
            raw_rsrc(src + first, __builtin_amdgcn_readfirstlane(max(min(left - first, 64), 0)) * 4));
     }
   };
@@ -391,15 +394,14 @@ __global__ void __launch_bounds__(256 * kS, 4 / kB) quest_gated_tiles_kernel(con
                                              min(n - row0, kTile), col0 + wn * 32 * kB, lane);
 }
 
-// Few rows (a decode step): the weights are the work, each read once, and a
-// 256 x 128 tile would leave most of the chip without any.  A workgroup takes
+// Few rows (a decode step): the weights are the work, each read once.  A workgroup takes
 // 16 kCt columns of h and all n <= 16 kT rows; its 8 waves take every 8th chunk
 // of 128 of k, straight from memory into the operand registers of the 16 x 16 x
 // 128 instruction (lane l: row l % 16, run l / 16 of the chunk, 24 bytes), and
 // add their exact sums through LDS.  kCt is 1, which gives the most workgroups,
 // or 2 where the 8-bit checkpoints need blocks of 32 columns in one place.
-// Bound by the latency of one pass over the weights: 1 x 2048 -> 5632 takes 5.4 us
-// (18.4 us with the 256 x 128 tiles), 17.4 MB.
+// Bound by the latency of one pass over the weights: 1 x 2048 -> 5632 takes 5.4 us, 48
+// rows 7.2 (7.8 with 64 x 64 tiles, whatever the rows), 17.4 MB.
 typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kFewWaves = 8;
 

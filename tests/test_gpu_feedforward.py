@@ -232,6 +232,37 @@ def test_calls_on_their_own_stream(dev):
             assert torch.equal(a, c)
 
 
+def test_two_streams_at_once(dev):
+    """The same calls in flight on two streams: each has its own workspace and outputs."""
+    log("two streams")
+    sets = []
+    for i in range(2):
+        x, dy = rand((3000, 1024), 40 + i, torch.bfloat16, dev), rand((3000, 1024), 50 + i, torch.bfloat16, dev)
+        w = rand((1024,), 60 + i, torch.float32, dev)
+        ops = [qa.quantize_fwd_op(rand((r, 1024), 70 + i, torch.bfloat16, dev), 128, 4) for r in (1024, 1024)]
+        sets.append((x, dy, w, ops))
+
+    def work(x, dy, w, ops, stream=None):
+        y, _, rstd, kept = qa.layer_norm_fwd(x, w, w, act8=True, stream=stream)
+        _, xs, _, xo = qa.quantize_fwd_op(x, 128, 4)
+        h, g8, u8 = qa.gated_fwd(xo, xs, 3000, 4, ops[0][3], ops[0][1], ops[1][3], ops[1][1], 1024, 4, 1024, act8=True,
+                                 stream=stream)
+        return (y, h, qa.gated_bwd(h, g8, u8, stream=stream),
+                *qa.layer_norm_bwd(dy, rstd, w, act8=kept, bias_grad=True, stream=stream))
+
+    want = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(work(*s, stream=st))
+        torch.cuda.synchronize()
+        for g, r in zip(got, want):
+            assert all(torch.equal(a, c) for a, c in zip(g, r))
+
+
 def test_gated_refusals(dev):
     log("refusals")
     x, w = rand((4, 256), 1, torch.bfloat16, dev), rand((8, 256), 2, torch.bfloat16, dev)
