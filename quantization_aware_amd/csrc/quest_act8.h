@@ -64,31 +64,91 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-// The same at any address that is a multiple of the element's size (global
-// memory takes wide accesses there at no more than the lines they touch), for
-// the `left` entries that a row has from there: 8 or more, a row's last few,
-// entry by entry (the others read as zero), or none.
+// The same at any address that is a multiple of the element's size: global
+// memory takes wide accesses there, at no more than the lines they touch.
+template <typename T>
+__device__ __forceinline__ void load8_at(const T* p, float (&v)[8]) {
+  typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+  const u32x4_u a = *reinterpret_cast<const u32x4_u*>(p);
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    }
+  } else {
+    const u32x4_u b = *reinterpret_cast<const u32x4_u*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8_at(T* p, const float (&v)[8]) {
+  typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<u32x4_u*>(p) =
+        u32x4_u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<u32x4_u*>(p + 4 * h) =
+          u32x4_u{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                  __float_as_uint(v[4 * h + 3])};
+  }
+}
+__device__ __forceinline__ uint2 load_codes8_at(const int8_t* p) {
+  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
+  const u32x2_u a = *reinterpret_cast<const u32x2_u*>(p);
+  return make_uint2(a[0], a[1]);
+}
+__device__ __forceinline__ void store_codes8_at(int8_t* p, uint2 w) {
+  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
+  *reinterpret_cast<u32x2_u*>(p) = u32x2_u{w.x, w.y};
+}
+
+// A group of 8 columns from c (a multiple of 8) of a row of `cols` >= 8 that is
+// no whole number of groups.  Every load is 8 wide and behind no branch: the
+// row's last group, and any past it, is taken `skip` entries early, so that it
+// ends with the row; its first `skip` entries belong to the group before (all 8
+// and more: no entry is its own) and count for nothing.
+struct Group {
+  int at, skip;
+  __device__ __forceinline__ Group(int c, int cols) : at(min(c, cols - 8)), skip(c - at) {}
+  __device__ __forceinline__ bool own(int i) const { return i >= skip; }
+};
+// Its own entries to memory (p: entry 0).
+template <typename T>
+__device__ __forceinline__ void store8_own(T* p, const Group& g, const float (&v)[8]) {
+  if (g.skip == 0) {
+    store8_at(p, v);
+  } else if (g.skip < 8) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= g.skip) p[i] = from_f32<T>(v[i]);
+  }
+}
+__device__ __forceinline__ void store_codes8_own(int8_t* p, const Group& g, uint2 w) {
+  if (g.skip == 0) {
+    store_codes8_at(p, w);
+  } else if (g.skip < 8) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= g.skip) p[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+  }
+}
+
+// For rows that may be narrower than a group: the `left` entries that a row has
+// from p on, 8 or more, a row's last few one by one (the others read as zero), or
+// none.
 template <typename T>
 __device__ __forceinline__ void load8_tail(const T* p, int left, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   if (left >= 8) {
-    typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
-    const u32x4_u a = *reinterpret_cast<const u32x4_u*>(p);
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(a[i] << 16);
-        v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-      }
-    } else {
-      const u32x4_u b = *reinterpret_cast<const u32x4_u*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(a[i]);
-        v[4 + i] = __uint_as_float(b[i]);
-      }
-    }
+    load8_at(p, v);
   } else if (left > 0) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -98,30 +158,17 @@ __device__ __forceinline__ void load8_tail(const T* p, int left, float (&v)[8]) 
 template <typename T>
 __device__ __forceinline__ void store8_tail(T* p, int left, const float (&v)[8]) {
   if (left >= 8) {
-    typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u32x4_u*>(p) =
-          u32x4_u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4_u*>(p + 4 * h) =
-            u32x4_u{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                    __float_as_uint(v[4 * h + 3])};
-    }
+    store8_at(p, v);
   } else if (left > 0) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
       if (i < left) p[i] = from_f32<T>(v[i]);
   }
 }
-// 8 codes likewise.
 __device__ __forceinline__ uint2 load_codes8_tail(const int8_t* p, int left) {
-  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
   uint2 w = make_uint2(0, 0);
   if (left >= 8) {
-    const u32x2_u a = *reinterpret_cast<const u32x2_u*>(p);
-    w = make_uint2(a[0], a[1]);
+    w = load_codes8_at(p);
   } else if (left > 0) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -130,9 +177,8 @@ __device__ __forceinline__ uint2 load_codes8_tail(const int8_t* p, int left) {
   return w;
 }
 __device__ __forceinline__ void store_codes8_tail(int8_t* p, int left, uint2 w) {
-  typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
   if (left >= 8) {
-    *reinterpret_cast<u32x2_u*>(p) = u32x2_u{w.x, w.y};
+    store_codes8_at(p, w);
   } else if (left > 0) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)

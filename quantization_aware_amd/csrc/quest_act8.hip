@@ -6,10 +6,12 @@
 // which entries 8 t .. 8 t + 7 belong to thread t: 16-byte accesses of bf16,
 // 8-byte accesses of codes, and a block is four neighbouring lanes, whose
 // maximum is two DPP steps.  Other widths keep those accesses at unaligned
-// addresses, four lanes a block, a row's last entries one by one; a workgroup
-// takes a run of consecutive blocks of the tensor, whatever rows they are of,
-// so narrow rows fill the waves as well as wide ones.  (8192 x 1001 bf16 is
-// saved in 8.4 us and read in 6.0; an entry an access took 12.5 and 10.6.)
+// addresses, four lanes a block, a row's last group ending with the row (Group in
+// quest_act8.h; rows narrower than 8 go entry by entry); a workgroup takes a run
+// of consecutive blocks of the tensor, whatever rows they are of, so narrow rows
+// fill the waves as well as wide ones.  (16384 x 5631 bf16 is saved in 54.4 us and
+// read in 53.7, as 5632 columns are; with a branch for the last entries in 75.5
+// and 62.5.)
 #include "quest_act8.h"
 
 #include "quest_launch.h"
@@ -60,7 +62,8 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kRun = kThreads / 4;  // blocks at a time
 
-template <typename T>
+// kGroups: rows of 8 columns and more.
+template <typename T, bool kGroups>
 __global__ void __launch_bounds__(kThreads)
     quest_act8_save_blocks_kernel(const T* __restrict__ x, int64_t total, int cols, int8_t* __restrict__ codes,
                                   uint8_t* __restrict__ scale) {
@@ -68,24 +71,36 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRun * kUnroll); first < total;
        first += static_cast<int64_t>(gridDim.x) * (kRun * kUnroll)) {
     const BlockRun run(first, cols);
+    const int last = static_cast<int>(min(total - 1 - first, static_cast<int64_t>(kRun * kUnroll - 1)));
     float v[kUnroll][8];
     int64_t at[kUnroll];
-    int left[kUnroll];  // entries of the row from there
+    int col[kUnroll];  // of the row; past it behind the tensor's last block
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       int64_t r;
       int b;
-      run.at(u * kRun + sub, r, b);
+      run.at(min(u * kRun + sub, last), r, b);
       const int c = b * kAct8Block + 8 * l;
-      left[u] = first + u * kRun + sub < total ? cols - c : 0;
-      at[u] = r * cols + c;
-      load8_tail(x + at[u], left[u], v[u]);
+      col[u] = u * kRun + sub <= last ? c : cols + 8;
+      if constexpr (kGroups) {
+        const Group g(col[u], cols);
+        at[u] = r * cols + g.at;
+        load8_at(x + at[u], v[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = g.own(i) ? v[u][i] : 0.0f;
+      } else {
+        at[u] = r * cols + c;
+        load8_tail(x + at[u], cols - col[u], v[u]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int e = static_cast<int>(quad_max(act8_mag8(v[u])) >> 23);
-      store_codes8_tail(codes + at[u], left[u], act8_encode8(v[u], e));
-      if (l == 0 && left[u] > 0) scale[first + u * kRun + sub] = static_cast<uint8_t>(e);
+      if constexpr (kGroups)
+        store_codes8_own(codes + at[u], Group(col[u], cols), act8_encode8(v[u], e));
+      else
+        store_codes8_tail(codes + at[u], cols - col[u], act8_encode8(v[u], e));
+      if (l == 0 && col[u] < cols) scale[first + u * kRun + sub] = static_cast<uint8_t>(e);
     }
   }
 }
@@ -115,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T>
+template <typename T, bool kGroups>
 __global__ void __launch_bounds__(kThreads)
     quest_act8_load_blocks_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scale, int64_t total,
                                   int cols, T* __restrict__ out) {
@@ -123,25 +138,35 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRun * kUnroll); first < total;
        first += static_cast<int64_t>(gridDim.x) * (kRun * kUnroll)) {
     const BlockRun run(first, cols);
+    const int last = static_cast<int>(min(total - 1 - first, static_cast<int64_t>(kRun * kUnroll - 1)));
     uint2 w[kUnroll];
-    int e[kUnroll], left[kUnroll];
+    int e[kUnroll], col[kUnroll];
     int64_t at[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       int64_t r;
       int b;
-      run.at(u * kRun + sub, r, b);
+      const int i = min(u * kRun + sub, last);
+      run.at(i, r, b);
       const int c = b * kAct8Block + 8 * l;
-      left[u] = first + u * kRun + sub < total ? cols - c : 0;
-      at[u] = r * cols + c;
-      e[u] = left[u] > 0 ? scale[first + u * kRun + sub] : 0;
-      w[u] = load_codes8_tail(codes + at[u], left[u]);
+      col[u] = u * kRun + sub <= last ? c : cols + 8;
+      e[u] = scale[first + i];
+      if constexpr (kGroups) {
+        at[u] = r * cols + Group(col[u], cols).at;
+        w[u] = load_codes8_at(codes + at[u]);
+      } else {
+        at[u] = r * cols + c;
+        w[u] = load_codes8_tail(codes + at[u], cols - col[u]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       float v[8];
       act8_decode8(w[u], e[u], v);
-      store8_tail(out + at[u], left[u], v);
+      if constexpr (kGroups)
+        store8_own(out + at[u], Group(col[u], cols), v);
+      else
+        store8_tail(out + at[u], cols - col[u], v);
     }
   }
 }
@@ -159,8 +184,10 @@ hipError_t save(const T* x, int64_t rows, int cols, int8_t* codes, uint8_t* scal
     const int64_t groups = rows * cols / 8, per = kThreads * kUnroll;
     hipLaunchKernelGGL(quest_act8_save_flat_kernel<T>, dim3(static_cast<uint32_t>((groups + per - 1) / per)),
                        dim3(kThreads), 0, stream, x, groups, codes, scale);
+  } else if (cols >= 8) {
+    hipLaunchKernelGGL((quest_act8_save_blocks_kernel<T, true>), dim3(block_grid(total)), dim3(kThreads), 0, stream, x, total, cols, codes, scale);
   } else {
-    hipLaunchKernelGGL(quest_act8_save_blocks_kernel<T>, dim3(block_grid(total)), dim3(kThreads), 0, stream, x, total, cols, codes, scale);
+    hipLaunchKernelGGL((quest_act8_save_blocks_kernel<T, false>), dim3(block_grid(total)), dim3(kThreads), 0, stream, x, total, cols, codes, scale);
   }
   return hipGetLastError();
 }
@@ -172,8 +199,10 @@ hipError_t load(const int8_t* codes, const uint8_t* scale, int64_t rows, int col
     const int64_t groups = rows * cols / 8, per = kThreads * kUnroll;
     hipLaunchKernelGGL(quest_act8_load_flat_kernel<T>, dim3(static_cast<uint32_t>((groups + per - 1) / per)),
                        dim3(kThreads), 0, stream, codes, scale, groups, out);
+  } else if (cols >= 8) {
+    hipLaunchKernelGGL((quest_act8_load_blocks_kernel<T, true>), dim3(block_grid(total)), dim3(kThreads), 0, stream, codes, scale, total, cols, out);
   } else {
-    hipLaunchKernelGGL(quest_act8_load_blocks_kernel<T>, dim3(block_grid(total)), dim3(kThreads), 0, stream, codes, scale, total, cols, out);
+    hipLaunchKernelGGL((quest_act8_load_blocks_kernel<T, false>), dim3(block_grid(total)), dim3(kThreads), 0, stream, codes, scale, total, cols, out);
   }
   return hipGetLastError();
 }

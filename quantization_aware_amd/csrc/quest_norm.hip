@@ -86,8 +86,10 @@ __device__ __forceinline__ int column(int t, int j) {
 
 // A row, or a parameter vector.  kVec (cols a multiple of 8): as a buffer
 // resource, whose accesses past the end read zero and write nothing, so that no
-// load or store stands behind a branch.  Otherwise by address, with the row's
-// last entries one by one.
+// load or store stands behind a branch.  Otherwise by address, in groups whose
+// last ends with the row (quest_act8.h; 16384 x 2047 backward 44.6 us, 40.1 for 2048
+// columns, 82 with a branch for the last entries); rows of 16 threads, which may
+// be narrower than a group, entry by entry at their end.
 struct Row {
   __amdgpu_buffer_rsrc_t rsrc;
   uintptr_t at;
@@ -101,14 +103,26 @@ __device__ __forceinline__ Row row_at(const void* p, int64_t row, int cols) {
           at, cols};
 }
 
+// How group j of thread t stands to the row: kClamped, by Group.
+template <int TPR, bool kVec>
+constexpr bool kClamped = !kVec && TPR >= 64;
+template <int TPR, bool kVec>
+__device__ __forceinline__ bool inside(int t, int j, int i, int cols) {
+  const int c = column<TPR>(t, j);
+  if constexpr (kClamped<TPR, kVec>) return Group(c, cols).own(i);
+  return c + i < cols;
+}
+
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 8 entries of a row of T in group j of thread t; zeros past its end.
+// 8 entries of a row of T in group j of thread t; only those `inside` count.
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void fetch(const Row& r, int t, int j, float (&v)[8]) {
   const int c = column<TPR>(t, j);
-  if constexpr (!kVec) {
+  if constexpr (kClamped<TPR, kVec>) {
+    load8_at(reinterpret_cast<const T*>(r.at) + Group(c, r.cols).at, v);
+  } else if constexpr (!kVec) {
     load8_tail(reinterpret_cast<const T*>(r.at) + c, r.cols - c, v);
   } else if constexpr (sizeof(T) == 2) {
     const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, c * 2, 0, 0);
@@ -130,7 +144,10 @@ __device__ __forceinline__ void fetch(const Row& r, int t, int j, float (&v)[8])
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)[8]) {
   const int c = column<TPR>(t, j);
-  if constexpr (!kVec) {
+  if constexpr (kClamped<TPR, kVec>) {
+    const Group g(c, r.cols);
+    store8_own(reinterpret_cast<T*>(r.at) + g.at, g, v);
+  } else if constexpr (!kVec) {
     store8_tail(reinterpret_cast<T*>(r.at) + c, r.cols - c, v);
   } else if constexpr (sizeof(T) == 2) {
     const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
@@ -144,16 +161,21 @@ __device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)
     }
   }
 }
-// The 8-bit checkpoint of such a group: a block is four neighbouring threads.
+// The 8-bit checkpoint of such a group (0 where it is not inside): a block is four
+// neighbouring threads.
 template <int TPR, bool kVec>
 __device__ __forceinline__ void put_act8(const Row& codes, const Row& scale, int t, int j, const float (&v)[8]) {
   const int c = column<TPR>(t, j);
   const int e = static_cast<int>(quad_max(act8_mag8(v)) >> 23);
   const uint2 w = act8_encode8(v, e);
-  if constexpr (kVec)
+  if constexpr (kVec) {
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{w.x, w.y}, codes.rsrc, c, 0, 0);
-  else
+  } else if constexpr (kClamped<TPR, kVec>) {
+    const Group g(c, codes.cols);
+    store_codes8_own(reinterpret_cast<int8_t*>(codes.at) + g.at, g, w);
+  } else {
     store_codes8_tail(reinterpret_cast<int8_t*>(codes.at) + c, codes.cols - c, w);
+  }
   if ((t & 3) == 0 && c < codes.cols) reinterpret_cast<uint8_t*>(scale.at)[c >> 5] = static_cast<uint8_t>(e);
 }
 // Parameters of either type.
@@ -211,7 +233,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += v[j][i];
+      for (int i = 0; i < 8; ++i)
+        sum += !kClamped<TPR, kVec> || inside<TPR, kVec>(t, j, i, cols) ? v[j][i] : 0.0f;
     row_sum2<TPR>(sum, none, part);
     const float near = sum / count;  // the mean, within the rounding of the sum
     float sq = 0.0f, off = 0.0f;
@@ -219,7 +242,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[j][i] = column<TPR>(t, j) + i < cols ? v[j][i] - near : 0.0f;
+        v[j][i] = inside<TPR, kVec>(t, j, i, cols) ? v[j][i] - near : 0.0f;
         off += v[j][i];
         sq = fmaf(v[j][i], v[j][i], sq);
       }
@@ -255,7 +278,7 @@ struct XhatRow {
   Row x, scale;
   float mean, rstd;
 };
-// 8 entries of xhat; entries past the row are not meant to be used.
+// 8 entries of xhat; only those `inside` are meant.
 template <typename T, int TPR, bool kVec, bool kAct8>
 __device__ __forceinline__ void fetch_xhat(const XhatRow& r, int t, int j, float (&v)[8]) {
   if constexpr (!kAct8) {
@@ -270,6 +293,9 @@ __device__ __forceinline__ void fetch_xhat(const XhatRow& r, int t, int j, float
       const u32x2 q = __builtin_amdgcn_raw_buffer_load_b64(r.x.rsrc, c, 0, 0);
       w = make_uint2(q[0], q[1]);
       e = __builtin_amdgcn_raw_buffer_load_b8(r.scale.rsrc, c >> 5, 0, 0);
+    } else if constexpr (kClamped<TPR, kVec>) {
+      w = load_codes8_at(reinterpret_cast<const int8_t*>(r.x.at) + Group(c, r.x.cols).at);
+      e = reinterpret_cast<const uint8_t*>(r.scale.at)[min(c, r.x.cols - 1) >> 5];
     } else {
       w = load_codes8_tail(reinterpret_cast<const int8_t*>(r.x.at) + c, r.x.cols - c);
       if (c < r.x.cols) e = reinterpret_cast<const uint8_t*>(r.scale.at)[c >> 5];
@@ -337,7 +363,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
       fetch<T, TPR, kVec>(dy, t, j, g[j]);
       fetch_xhat<T, TPR, kVec, kAct8>(xr, t, j, xh[j]);
     }
-    // Places past the row count as zero.
+    // Entries that are not the group's own count as zero.
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -345,8 +371,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
       if constexpr (!kParams || kWide) weight(j, w[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = column<TPR>(t, j) + i < cols;
-        const float d = g[j][i], x = in ? xh[j][i] : 0.0f;
+        const bool in = inside<TPR, kVec>(t, j, i, cols);
+        const float d = in ? g[j][i] : 0.0f, x = in ? xh[j][i] : 0.0f;
         if constexpr (kParams) {
           if constexpr (kWide)
             sums[(8 * j + i) * TPR + t] += d * x;
@@ -433,8 +459,9 @@ __global__ void __launch_bounds__(256) quest_norm_colsum_kernel(const NormBwdLau
     fetch_xhat<T, 256, kVec, kAct8>(xhat_row<T, kAct8>(a, row), t, j, xh);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      dw[i] = fmaf(g[i], xh[i], dw[i]);
-      db[i] += g[i];
+      const bool in = inside<256, kVec>(t, j, i, cols);
+      dw[i] = in ? fmaf(g[i], xh[i], dw[i]) : 0.0f;
+      db[i] += in ? g[i] : 0.0f;
     }
   }
   put<float, 256, kVec>(row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.y), cols), t, j, dw);
