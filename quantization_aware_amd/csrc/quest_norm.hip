@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = inside<TPR, kVec>(t, j, i, cols);
-        const float d = in ? g[j][i] : 0.0f, x = in ? xh[j][i] : 0.0f;
+        // (only a clamped group's gradients reach past the row)
+        const float d = !kClamped<TPR, kVec> || in ? g[j][i] : 0.0f, x = in ? xh[j][i] : 0.0f;
         if constexpr (kParams) {
           if constexpr (kWide)
             sums[(8 * j + i) * TPR + t] += d * x;
