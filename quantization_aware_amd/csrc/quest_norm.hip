@@ -161,12 +161,19 @@ __device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)
     }
   }
 }
-// The 8-bit checkpoint of such a group (0 where it is not inside): a block is four
-// neighbouring threads.
+// The 8-bit checkpoint of such a group: a block is four neighbouring threads.  What
+// lies past the row in its last block has no part in the block's exponent.
 template <int TPR, bool kVec>
 __device__ __forceinline__ void put_act8(const Row& codes, const Row& scale, int t, int j, const float (&v)[8]) {
   const int c = column<TPR>(t, j);
-  const int e = static_cast<int>(quad_max(act8_mag8(v)) >> 23);
+  uint32_t mag = 0;
+  if constexpr (kVec) {
+    mag = c < codes.cols ? act8_mag8(v) : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mag = inside<TPR, kVec>(t, j, i, codes.cols) ? max(mag, act8_mag(v[i])) : mag;
+  }
+  const int e = static_cast<int>(quad_max(mag) >> 23);
   const uint2 w = act8_encode8(v, e);
   if constexpr (kVec) {
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{w.x, w.y}, codes.rsrc, c, 0, 0);

@@ -170,6 +170,22 @@ def test_bad_entries_stay_in_their_row(dev, bad):
     assert torch.isnan(dx[4]).all() and torch.isfinite(dx[keep]).all()
 
 
+@pytest.mark.parametrize("cols", [7, 19, 33, 100, 257, 700, 993, 1000, 1111, 2049, 5640, 9001, 16392, 20001])
+def test_checkpoint_is_that_of_the_normalised_input(dev, cols):
+    """Without parameters an fp32 y is xhat itself, so the checkpoint is the one that saving y gives, byte for byte:
+    rows of one value (zeros), and rows whose last block holds next to nothing, among them."""
+    log(f"checkpoint of {cols} columns")
+    g = torch.Generator().manual_seed(cols)
+    for rows in (6, 600):
+        x = torch.randn((rows, cols), generator=g) + 1000.3
+        x[0], x[1] = 0.1, -1e4 / 3
+        tail = cols - (cols - 1) // 32 * 32
+        x[2:4, -tail:] = x[2:4].mean(1, keepdim=True)
+        y, _, _, kept = run_fwd(dev, x, None, None, act8=True)
+        want = qa.act8_save(y)
+        assert torch.equal(kept[1], want[1]) and torch.equal(kept[0], want[0])
+
+
 def test_no_rows(dev):
     log("no rows")
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=dev)
