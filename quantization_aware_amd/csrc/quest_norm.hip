@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
     row_sum2<TPR>(sq, off, part);
     off /= count;  // what `near` missed
     const float mean = near + off;
-    const float rstd = 1.0f / sqrtf(fmaxf(sq / count - off * off, 0.0f) + a.eps);
+    const float var = sq / count - off * off;
+    const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);  // (NaN stays)
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;

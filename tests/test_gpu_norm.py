@@ -186,6 +186,20 @@ def test_checkpoint_is_that_of_the_normalised_input(dev, cols):
         assert torch.equal(kept[1], want[1]) and torch.equal(kept[0], want[0])
 
 
+@pytest.mark.parametrize("cols", [19, 700, 1111, 9001])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_statistics_of_bad_rows(dev, cols, bad):
+    """A row with an infinity or NaN has no finite statistics, wherever it lies."""
+    log(f"{bad} in {cols} columns")
+    for at in (0, cols - 1):
+        x, _, w, b = inputs(5, cols, torch.float32, torch.float32, 8)
+        x[2, at] = bad
+        y, mean, rstd, _ = run_fwd(dev, x, w, b)
+        assert torch.isnan(y[2]).all() and torch.isnan(rstd[2]) and not torch.isfinite(mean[2])
+        keep = [0, 1, 3, 4]
+        assert torch.isfinite(y[keep]).all() and torch.isfinite(rstd[keep]).all()
+
+
 def test_no_rows(dev):
     log("no rows")
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=dev)
