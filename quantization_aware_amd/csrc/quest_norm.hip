@@ -478,11 +478,11 @@ __global__ void __launch_bounds__(256) quest_norm_colsum_kernel(const NormBwdLau
 }
 
 // The workgroups' column sums added in a fixed order: slice s of a workgroup
-// adds every 16th of them from s for its 32 columns, 8 loads at a time, then
-// the slices are added.  Few columns a workgroup and many loads in flight:
-// the sums of 512 workgroups over 2048 columns take 4.2 us (31 us with 4 slices
+// adds every 16th of them from s for its 32 columns, 16 loads at a time (the last few
+// 8 at a time), then the slices are added.  Few columns a workgroup and many loads in
+// flight: the sums of 512 workgroups over 2048 columns take 4.2 us (31 us with 4 slices
 // of 64 columns and one load at a time, all of it latency).
-constexpr int kSlices = 16, kSumCols = 32;
+constexpr int kSlices = 16, kSumCols = 32, kLoads = 16;
 template <typename P>
 __global__ void __launch_bounds__(kSlices* kSumCols)
     quest_norm_params_kernel(const float* __restrict__ ws, int groups, int cols, P* __restrict__ dw,
@@ -495,14 +495,20 @@ __global__ void __launch_bounds__(kSlices* kSumCols)
     const float* p = ws + c;
     const int64_t pitch = 2 * static_cast<int64_t>(cols);
     int g = s;
-    for (; g + 7 * kSlices < groups; g += 8 * kSlices) {
+    for (; g + (kLoads - 1) * kSlices < groups; g += kLoads * kSlices) {
+      float x[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) x[i] = p[(g + i * kSlices) * pitch];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) v += x[i];
+    }
+    for (; g < groups; g += 8 * kSlices) {  // the rest: 8 loads together as well
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = p[(g + i * kSlices) * pitch];
+      for (int i = 0; i < 8; ++i) x[i] = p[min(g + i * kSlices, groups - 1) * pitch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v += x[i];
+      for (int i = 0; i < 8; ++i) v += g + i * kSlices < groups ? x[i] : 0.0f;
     }
-    for (; g < groups; g += kSlices) v += p[g * pitch];
   }
   part[s][lane] = v;
   __syncthreads();
@@ -521,12 +527,17 @@ __global__ void __launch_bounds__(kSlices* kSumCols)
 // stores of y are ordinary ones: non-temporal they make the norm alone faster
 // (23.1 us), but not with the quantiser that reads y next (49.0 us both, 47.6 so).
 constexpr int kMaxFwdBlocks = 2048;
-// Up to so many rows of 513 to 2048 columns (a row for each of the backward's
-// workgroups) a row has a workgroup's 256 threads and not a wave's 64, whose chain
-// of loads and sums is what such a call takes: 1 x 2048 forward 2.4 us against 3.8,
-// backward 2.4 against 5.4; 256 x 2048 3.4 against 5.0 and 5.1 against 6.9; at 1000
-// rows the backward of 1024 columns would take 7.5 against 5.4.
-constexpr int kFewRows = 512;
+// Rows of 513 to 2048 columns that have a workgroup's 256 threads and not a wave's 64,
+// whose chain of loads and sums is what a call of few rows takes.  Us with 256 and with 64
+// (the backward's with the sums added): forward, bf16, 1 x 2048 2.4 and 3.8, 768 x 2048 3.8
+// and 4.0, 1500 x 2048 5.3 and 5.0; fp32 8192 x 2048 22.4 and 23.2, 16384 x 1111 27.9 and
+// 27.6; up to 1024 columns 256 x 600 3.1 and 3.0.  Backward, 1500 x 2048 bf16 12.2 and 12.8,
+// fp32 13.4 and 14.7; 4096 x 2048 16.0 and 16.6, 18.1 and 20.4; 6000 x 2048 19.4 and 18.2,
+// 22.7 and 24.8; 256 x 600 5.6 and 6.2, 400 x 600 7.0 and 6.3.
+constexpr bool few_fwd(int64_t rows, int cols, bool f32) {
+  return cols > 1024 ? rows <= (f32 ? 8192 : 768) : rows <= 256;
+}
+constexpr bool few_bwd(int64_t rows, int64_t cols) { return cols > 1024 ? rows <= 4096 : rows <= 256; }
 // Rows of 16 threads: 111661 x 19 forward 13.5 us, 49.5 with a wave a row; backward 23.7
 // and 49.2.
 constexpr int kNarrowCols = 128;
@@ -548,7 +559,7 @@ template <typename T, bool kVec>
 hipError_t fwd_width(const NormFwdLaunch& a) {
   if (a.cols <= kNarrowCols) return fwd<T, 16, 1, false>(a);
   if (a.cols <= 512) return fwd<T, 64, 1, kVec>(a);
-  if (a.rows <= kFewRows && a.cols <= 2048) return fwd<T, 256, 1, kVec>(a);
+  if (a.cols <= 2048 && few_fwd(a.rows, a.cols, sizeof(T) == 4)) return fwd<T, 256, 1, kVec>(a);
   if (a.cols <= 1024) return fwd<T, 64, 2, kVec>(a);
   if (a.cols <= 2048) return fwd<T, 64, 4, kVec>(a);
   if (a.cols <= 4096) return fwd<T, 256, 2, kVec>(a);
@@ -581,7 +592,7 @@ hipError_t bwd_width(const NormBwdLaunch& a, int groups) {
   } else if (a.workspace) {
     if (a.cols <= kNarrowCols) return bwd<T, 16, 1, false, true>(a, groups);
     if (a.cols <= 512) return bwd<T, 64, 1, kVec, true>(a, groups);
-    if (a.rows <= kFewRows && a.cols <= 2048) return bwd<T, 256, 1, kVec, true>(a, groups);
+    if (a.cols <= 2048 && few_bwd(a.rows, a.cols)) return bwd<T, 256, 1, kVec, true>(a, groups);
     if (a.cols <= 1024) return bwd<T, 64, 2, kVec, true>(a, groups);
     if (a.cols <= 2048) return bwd<T, 64, 4, kVec, true>(a, groups);
     if (a.cols <= 4096) return bwd<T, 256, 2, kVec, true>(a, groups);
@@ -608,11 +619,18 @@ hipError_t launch_norm_fwd(const NormFwdLaunch& a, bool x_bf16) {
 
 int norm_bwd_groups(int64_t rows, int64_t cols) {
   // rows a workgroup holds at a time
-  const int64_t per = cols <= kNarrowCols ? 16 : cols <= 512 || (cols <= 2048 && rows > kFewRows) ? 4 : 1;
-  // as many workgroups as fit the chip by their registers, or as their sums are
-  // soon added
-  const int64_t n = (rows + per - 1) / per, most = cols <= kNarrowCols ? 1024 : cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;
-  return static_cast<int>(n < most ? n : most);
+  const int64_t per = cols <= kNarrowCols ? 16 : cols <= 512 || (cols <= 2048 && !few_bwd(rows, cols)) ? 4 : 1;
+  // Workgroups: few enough that adding their sums is short, until the rows fill the chip
+  // (1000 x 1111 fp32 in 250 and 256 x 8192 bf16 in 128: 9.6 and 13.0 us both kernels, 10.5
+  // and 15.7 with up to 512; 4096 x 1024 bf16 in 256 10.3, 13.6 with 1024); then as many as
+  // fit it by their registers, or as their sums are soon added.
+  const int64_t n = (rows + per - 1) / per;
+  const int64_t fit = cols <= kNarrowCols ? 1024 : cols <= 512 ? 2048 : cols <= 1024 ? 1024 : cols <= 8192 ? 512 : 256;
+  const int64_t most = n <= 256 ? 128 : n <= 2048 ? 256 : fit;
+  if (n == 0) return 0;
+  // (and no more of them than the busiest one's share of the rows needs)
+  const int64_t turns = (n + most - 1) / most;
+  return static_cast<int>((n + turns - 1) / turns);
 }
 
 hipError_t launch_norm_bwd(const NormBwdLaunch& a, bool bf16) {

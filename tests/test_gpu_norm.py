@@ -122,6 +122,15 @@ def test_backward_without_weight(dev):
     fo.check("db", db, fo.norm_bwd(*args)[2], fo.norm_bwd_bounds(*args)[2])
 
 
+@pytest.mark.parametrize("rows,cols", [(8193, 1111), (8200, 1032), (4097, 1500), (2049, 600), (1025, 2049), (300, 5631)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_past_the_few(dev, rows, cols, dtype):
+    """Either side of the numbers of rows at which rows are given to fewer threads, or sums to fewer workgroups."""
+    test_forward(dev, rows, cols, dtype, torch.float32)
+    test_backward(dev, rows, cols, dtype, torch.float32, False)
+    test_backward(dev, rows, cols, dtype, torch.bfloat16, True)
+
+
 def test_many_rows(dev):
     """More rows than workgroups walk at once, few columns."""
     log("300000x24")
