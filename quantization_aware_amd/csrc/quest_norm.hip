@@ -87,7 +87,7 @@ __device__ __forceinline__ int column(int t, int j) {
 // A row, or a parameter vector.  kVec (cols a multiple of 8): as a buffer
 // resource, whose accesses past the end read zero and write nothing, so that no
 // load or store stands behind a branch.  Otherwise by address, in groups whose
-// last ends with the row (quest_act8.h; 16384 x 2047 backward 44.6 us, 40.1 for 2048
+// last ends with the row (quest_act8.h; 16384 x 2047 backward 43.3 us, 40.1 for 2048
 // columns, 82 with a branch for the last entries); rows of 16 threads, which may
 // be narrower than a group, entry by entry at their end.
 struct Row {
@@ -111,6 +111,18 @@ __device__ __forceinline__ bool inside(int t, int j, int i, int cols) {
   const int c = column<TPR>(t, j);
   if constexpr (kClamped<TPR, kVec>) return Group(c, cols).own(i);
   return c + i < cols;
+}
+
+// Entries that are not the group's own as zeros.  Of a row's waves only the last and
+// those past it have any: the others pass by on a scalar branch (8000 x 5631 forward
+// 46 us, 57 with a select at every entry).
+template <int TPR, bool kVec>
+__device__ __forceinline__ void own_only(int t, int j, int cols, float (&v)[8]) {
+  if constexpr (TPR >= 64) {
+    if (column<TPR>(__builtin_amdgcn_readfirstlane(t), j) + 8 * 64 <= cols) return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = inside<TPR, kVec>(t, j, i, cols) ? v[i] : 0.0f;
 }
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -162,17 +174,12 @@ __device__ __forceinline__ void put(const Row& r, int t, int j, const float (&v)
   }
 }
 // The 8-bit checkpoint of such a group: a block is four neighbouring threads.  What
-// lies past the row in its last block has no part in the block's exponent.
+// lies past the row in its last block has no part in the block's exponent (without
+// kVec: v is zero there).
 template <int TPR, bool kVec>
 __device__ __forceinline__ void put_act8(const Row& codes, const Row& scale, int t, int j, const float (&v)[8]) {
   const int c = column<TPR>(t, j);
-  uint32_t mag = 0;
-  if constexpr (kVec) {
-    mag = c < codes.cols ? act8_mag8(v) : 0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mag = inside<TPR, kVec>(t, j, i, codes.cols) ? max(mag, act8_mag(v[i])) : mag;
-  }
+  const uint32_t mag = !kVec || c < codes.cols ? act8_mag8(v) : 0;
   const int e = static_cast<int>(quad_max(mag) >> 23);
   const uint2 w = act8_encode8(v, e);
   if constexpr (kVec) {
@@ -238,21 +245,26 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
 #pragma unroll
     for (int j = 0; j < NC; ++j) fetch<T, TPR, kVec>(x, t, j, v[j]);
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < NC; ++j) {
+      if constexpr (kClamped<TPR, kVec>) own_only<TPR, kVec>(t, j, cols, v[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sum += !kClamped<TPR, kVec> || inside<TPR, kVec>(t, j, i, cols) ? v[j][i] : 0.0f;
+      for (int i = 0; i < 8; ++i) sum += v[j][i];
+    }
     row_sum2<TPR>(sum, none, part);
     const float near = sum / count;  // the mean, within the rounding of the sum
     float sq = 0.0f, off = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < NC; ++j) {
+      const bool in = !kVec || column<TPR>(t, j) < cols;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = in ? v[j][i] - near : 0.0f;
+      if constexpr (!kVec) own_only<TPR, kVec>(t, j, cols, v[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[j][i] = inside<TPR, kVec>(t, j, i, cols) ? v[j][i] - near : 0.0f;
         off += v[j][i];
         sq = fmaf(v[j][i], v[j][i], sq);
       }
+    }
     row_sum2<TPR>(sq, off, part);
     off /= count;  // what `near` missed
     const float mean = near + off;
@@ -275,6 +287,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
       }
       put<T, TPR, kVec>(y, t, j, o);
       if (a.codes) {
+        if constexpr (!kVec) own_only<TPR, kVec>(t, j, cols, v[j]);
         put_act8<TPR, kVec>(row_at<int8_t>(a.codes, row, cols), row_at<uint8_t>(a.scale, row, blocks), t, j, v[j]);
       }
     }
@@ -335,6 +348,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
   // each thread's its own, and the weight read again from the caches for every row
   // (2048 x 16384 bf16: 54.8 us, 67.2 with 512 threads and all in registers).
   constexpr bool kWide = kParams && TPR == 1024;
+  constexpr bool kSkip = kParams && kClamped<TPR, kVec>;
   constexpr int kSums = kWide ? 8 * NC * TPR : kParams && kRows > 1 ? 2 * 8 * NC * TPR : 1;
   constexpr int kHeld = kParams ? NC : 1, kHeldW = kParams && !kWide ? NC : 1;
   __shared__ float part[TPR > 64 ? 2 * TPR / 64 : 1];
@@ -348,6 +362,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 1.0f;
     if (a.weight) fetch_param<TPR, kVec>(a.weight, a.param_bf16, cols, t, j, v);
+    if constexpr (kSkip) own_only<TPR, kVec>(t, j, cols, v);
   };
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
@@ -371,16 +386,22 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_bwd_kernel(cons
       fetch<T, TPR, kVec>(dy, t, j, g[j]);
       fetch_xhat<T, TPR, kVec, kAct8>(xr, t, j, xh[j]);
     }
-    // Entries that are not the group's own count as zero.
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int held = kHeldW > 1 ? j : 0;
       if constexpr (!kParams || kWide) weight(j, w[0]);
+      // Entries that are not the group's own count as zero: by own_only where that is the
+      // faster (16384 x 2047 from the 8-bit copy 40.7 us, 46.6 with a select at each; 2048
+      // columns 36.5 with selects and 48 without; dx alone of 8000 x 5631 69 and 76).
+      // Only a clamped group's gradients and weights reach past the row.
+      if constexpr (kSkip) {
+        own_only<TPR, kVec>(t, j, cols, g[j]);
+        own_only<TPR, kVec>(t, j, cols, xh[j]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = inside<TPR, kVec>(t, j, i, cols);
-        // (only a clamped group's gradients reach past the row)
+        const bool in = kSkip || inside<TPR, kVec>(t, j, i, cols);
         const float d = !kClamped<TPR, kVec> || in ? g[j][i] : 0.0f, x = in ? xh[j][i] : 0.0f;
         if constexpr (kParams) {
           if constexpr (kWide)
@@ -466,11 +487,11 @@ __global__ void __launch_bounds__(256) quest_norm_colsum_kernel(const NormBwdLau
     float g[8], xh[8];
     fetch<T, 256, kVec>(row_at<T>(a.dy, row, cols), t, j, g);
     fetch_xhat<T, 256, kVec, kAct8>(xhat_row<T, kAct8>(a, row), t, j, xh);
+    // (what is not the group's own is not stored)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool in = inside<256, kVec>(t, j, i, cols);
-      dw[i] = in ? fmaf(g[i], xh[i], dw[i]) : 0.0f;
-      db[i] += in ? g[i] : 0.0f;
+      dw[i] = fmaf(g[i], xh[i], dw[i]);
+      db[i] += g[i];
     }
   }
   put<float, 256, kVec>(row_at<float>(a.workspace, 2 * static_cast<int64_t>(blockIdx.y), cols), t, j, dw);
@@ -606,6 +627,7 @@ hipError_t bwd_width(const NormBwdLaunch& a, int groups) {
   if (a.cols <= 512) return bwd<T, 64, 1, kVec, false>(a, groups);
   if (a.cols <= 2048) return bwd<T, 64, 4, kVec, false>(a, groups);
   if (a.cols <= 8192) return bwd<T, 256, 4, kVec, false>(a, groups);
+  if (a.cols <= 16384) return bwd<T, 1024, 2, kVec, false>(a, groups);
   return bwd<T, 1024, 4, kVec, false>(a, groups);
 }
 
