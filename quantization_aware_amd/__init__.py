@@ -740,8 +740,8 @@ def _act8_specs(name: str, pair, rows: int, cols: int):
 
 
 def _new_act8(rows: int, cols: int, device):
-    return (torch.empty((rows, cols), dtype=torch.int8, device=device),
-            torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=device))
+    return (torch.empty(rows, cols, dtype=torch.int8, device=device),
+            torch.empty(rows, -(-cols // 32), dtype=torch.uint8, device=device))
 
 
 def act8_save(x: torch.Tensor, codes=None, scale=None, stream=None):
@@ -782,7 +782,7 @@ def act8_load(codes: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16
     specs = _act8_specs("the checkpoint's", (codes, scale), rows, cols)
     if out is None:
         code = _float_code(out_dtype)
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        out = torch.empty(rows, cols, dtype=out_dtype, device=dev)
     else:
         code = _matrix("out", out)
         specs += (("out", out, out.dtype, (rows, cols)),)
@@ -828,7 +828,7 @@ def layer_norm_fwd(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, a
     _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty_like(x)
-    mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     codes, scale = _new_act8(rows, cols, dev) if act8 else (None, None)
     _launch("quest_layer_norm_fwd", dev, x.data_ptr(), code, rows, cols, _ptr(weight), _ptr(bias),
@@ -871,12 +871,12 @@ def layer_norm_bwd(dy: torch.Tensor, rstd: torch.Tensor, weight=None, *, x=None,
         raise TypeError(f"parameter gradients are float32 or bfloat16, not {param_dtype}")
     _check_tensors(dev, ("dy", dy, dy.dtype, None), ("rstd", rstd, torch.float32, (rows,)), *source, *params)
     dx = torch.empty_like(dy) if input_grad else None
-    dweight = torch.empty((cols,), dtype=param_dtype, device=dev) if weight_grad else None
-    dbias = torch.empty((cols,), dtype=param_dtype, device=dev) if bias_grad else None
+    dweight = torch.empty(cols, dtype=param_dtype, device=dev) if weight_grad else None
+    dbias = torch.empty(cols, dtype=param_dtype, device=dev) if bias_grad else None
     ws = None
     if weight_grad or bias_grad:
         need = int(load_library().quest_layer_norm_workspace_bytes(rows, cols))
-        ws = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _launch("quest_layer_norm_bwd", dev, dy.data_ptr(), code, rows, cols, _ptr(x), _ptr(mean),
             _ptr(codes), _ptr(scale), rstd.data_ptr(), _ptr(weight),
             QUEST_BF16 if param_dtype == torch.bfloat16 else QUEST_F32, _ptr(dx), _ptr(dweight), _ptr(dbias),
@@ -922,7 +922,7 @@ def gated_fwd(x: torch.Tensor, x_scale: torch.Tensor, n: int, x_bits: int, gate:
         specs += (("out", out, out.dtype, (n, m)),)
     _check_tensors(dev, *specs)
     if out is None:
-        out = torch.empty((n, m), dtype=out_dtype, device=dev)
+        out = torch.empty(n, m, dtype=out_dtype, device=dev)
     gate8 = _new_act8(n, m, dev) if act8 else (None, None)
     up8 = _new_act8(n, m, dev) if act8 else (None, None)
     _launch("quest_gated_fwd", dev, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), gate.data_ptr(),
@@ -949,7 +949,7 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
         specs += (("out", out, dh.dtype, (rows, 2 * cols)),)
     _check_tensors(dev, *specs)
     if out is None:
-        out = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dev)
+        out = torch.empty(rows, 2 * cols, dtype=dh.dtype, device=dev)
     _launch("quest_gated_bwd", dev, dh.data_ptr(), code, rows, cols, gate8[0].data_ptr(), gate8[1].data_ptr(),
             up8[0].data_ptr(), up8[1].data_ptr(), act_code, out.data_ptr())
     return out
