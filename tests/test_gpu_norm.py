@@ -151,6 +151,27 @@ def test_large_offset_keeps_its_digits(dev):
     check_fwd(run_fwd(dev, x, w, b), x, w, b)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(64, 100), (40, 500), (100, 1111), (300, 1000), (64, 2048), (9000, 2048), (9000, 1111),
+                                       (40, 4096), (33, 5631), (9, 16384), (5, 20001)])
+def test_mean_of_an_exact_sum(dev, rows, cols, dtype):
+    """Entries of a coarse grid, whose fp32 sum is exact in any order (whole multiples of 2^-6 below 2^17): the first
+    sum gives the mean correctly rounded, and the roundings of x - mean are not taken for a part of it.  They are at
+    most U |x - mean| each, U a quarter to a half of the entries' rms on average here; the sum's own rounding adds
+    about U rms (64 / cols)^(1/2) or less."""
+    log(f"exact sums {rows}x{cols} {dtype}")
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn((rows, cols), generator=g) + 0.1
+    x[:, 5::100] *= 16
+    x = (torch.round(x * 64) / 64).to(dtype)
+    x64 = fo.f64(x)
+    assert np.abs(x64).sum(axis=1).max() < 2 ** 17
+    _, mean, _, _ = run_fwd(dev, x, None, None)
+    want = (x64.sum(axis=1) / cols).astype(np.float32)
+    off = (mean.cpu().numpy() != want)
+    assert not off.any(), f"{off.sum()} of {rows} means are not the correctly rounded ones"
+
+
 def test_constant_and_zero_rows(dev):
     log("constant rows")
     x = torch.zeros((4, 257))
