@@ -225,8 +225,8 @@ __device__ __forceinline__ uint32_t act8_mag8(const float (&v)[8]) {
   return a;
 }
 
-// Four finite entries, packed: adding 1.5 * 2^23 rounds to a whole number
-// (nearest even) and leaves its low byte, in two's complement, lowest.
+// Four entries, packed: adding 1.5 * 2^23 rounds to a whole number (nearest
+// even) and leaves its low byte, in two's complement, lowest.
 __device__ __forceinline__ uint32_t act8_encode4(float a, float b, float c, float d, int e) {
   const float in[4] = {a, b, c, d};
   uint32_t w[4];
@@ -234,7 +234,7 @@ __device__ __forceinline__ uint32_t act8_encode4(float a, float b, float c, floa
   for (int i = 0; i < 4; ++i)
     w[i] = __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_ldexpf(in[i], 133 - e), -127.0f, 127.0f) + 12582912.0f);
   const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0400), hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000C0C);
-  return lo | hi;
+  return e == 255 ? 0u : lo | hi;
 }
 
 // max over the lanes of an aligned group of 4 (quad) or 32 lanes (half wave).

@@ -148,8 +148,8 @@ __device__ __forceinline__ void gated_epilogue(const GatedLaunch& a, v16f (&acc)
           if constexpr (kAct8) {
             acc[jj][i][4 * q + e] = gv;
             acc[kB + jj][i][4 * q + e] = uv;
-            mg = fmaxf(mg, fabsf(gv));
-            mu = fmaxf(mu, fabsf(uv));
+            mg = __builtin_elementwise_maximum(mg, fabsf(gv));  // (NaN stays, as in act8_mag's order)
+            mu = __builtin_elementwise_maximum(mu, fabsf(uv));
           }
         }
         uint8_t* d = slab + r32 * kPitch + cl * kOut;

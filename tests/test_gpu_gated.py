@@ -92,6 +92,33 @@ def test_wide_values(dev, act):
         fo.check("h", h, want, err + 2.0 ** -126 * (1 + np.abs(ops[0][2].times(ops[2][2]))))
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("n,k,m", [(40, 256, 200), (64, 128, 96), (65, 128, 96), (300, 256, 200), (300, 128, 208),
+                                   (70, 4224, 150), (2309, 128, 2320), (2305, 128, 2317)])
+def test_checkpoints_of_bad_products(dev, n, k, m, act):
+    """Clip scales with infinities, NaN and values whose products overflow: the checkpoints are those that the products
+    give when they are saved (a block with such an entry: exponent 255, codes 0), at every number of rows, and the
+    backward pass gives NaN in those blocks and nowhere else."""
+    log(f"bad products {n}x{k}x{m} {act}")
+    (xo, xs, _), (go, gs, _), (uo, us, _) = case(dev, n, k, m, 4, 4, seed=n + m)
+    xs, gs, us = xs.clone(), gs.clone(), us.clone()
+    xs[3], xs[n - 1], xs[n // 2] = float("nan"), float("inf"), 1e30
+    gs[5], gs[m - 1], us[40], us[m // 2] = float("nan"), 1e30, float("inf"), float("-inf")
+    _, g8, u8 = qa.gated_fwd(xo, xs, n, 4, go, gs, uo, us, m, 4, k, act=act, act8=True)
+    bad = []
+    for (codes, scale), wo, ws in ((g8, go, gs), (u8, uo, us)):
+        prod = qa.gemm(xo, xs, n, 4, wo, ws, m, 4, k, out_dtype=torch.float32)
+        c, s = qa.act8_save(prod)
+        assert torch.equal(scale, s) and torch.equal(codes, c)
+        bad.append(s == 255)
+        pad = torch.nn.functional.pad(~torch.isfinite(prod), (0, -m % 32)).reshape(n, -1, 32).any(2)
+        assert torch.equal(bad[-1], pad) and pad.any() and not pad.all()
+    wide = [b.repeat_interleave(32, dim=1)[:, :m] for b in bad]
+    dh = torch.full((n, m), 1e-3, device=dev)
+    out = qa.gated_bwd(dh, g8, u8, act=act)
+    assert torch.equal(torch.isnan(out), torch.cat([wide[0] | wide[1], wide[0]], 1))
+
+
 def test_zero_rows_and_shared_weights(dev):
     log("zero rows, gate and up one buffer")
     n, k, m = 20, 256, 48
