@@ -119,6 +119,31 @@ def test_checkpoints_of_bad_products(dev, n, k, m, act):
     assert torch.equal(torch.isnan(out), torch.cat([wide[0] | wide[1], wide[0]], 1))
 
 
+# (products of 128 x 128 tiles need five tiles for every four of the 256 compute units)
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("n,k,m,xb,wb", [(2309, 256, 2320, 4, 4), (2305, 384, 2317, 3, 4), (40961, 128, 65, 4, 4)])
+def test_forward_of_many_tiles(dev, n, k, m, xb, wb, act, out_dtype):
+    """Products large enough for the largest tiles, of widths with and without whole 16-byte chunks."""
+    log(f"many tiles {n}x{k}x{m} b={xb},{wb} {act} {out_dtype}")
+    ops = case(dev, n, k, m, xb, wb, seed=n + k + m)
+    h, _, _ = call(ops, n, k, m, xb, wb, act=act, out_dtype=out_dtype)
+    g, u = ops[0][2].times(ops[1][2]), ops[0][2].times(ops[2][2])
+    # fp32 roundings of a product: 2 / (2^b - 1) and its product with the clip scale for both operands, the product
+    # of the two, and that with the exact sum
+    dg, du = 6 * fo.U * np.abs(g), 6 * fo.U * np.abs(u)
+    v, slope, dv, _ = fo.act(g, act)
+    d_act = dv + np.abs(slope) * dg + dg * dg
+    r = fo.check("h", h, v * u, np.abs(u) * d_act + (np.abs(v) + d_act) * du + 2 * fo.U * np.abs(v * u))
+    log(f"error / tolerance {r:.3g}")
+    h2, g8, u8 = call(ops, n, k, m, xb, wb, act=act, out_dtype=out_dtype, act8=True)
+    assert torch.equal(h, h2)
+    for (codes, scale), exact, d, (wo, ws, _) in ((g8, g, dg, ops[1]), (u8, u, du, ops[2])):
+        fo.check_act8_of(codes.cpu().numpy(), scale.cpu().numpy(), exact, d)
+        c, s = qa.act8_save(qa.gemm(ops[0][0], ops[0][1], n, xb, wo, ws, m, wb, k, out_dtype=torch.float32))
+        assert torch.equal(codes, c) and torch.equal(scale, s)
+
+
 def test_zero_rows_and_shared_weights(dev):
     log("zero rows, gate and up one buffer")
     n, k, m = 20, 256, 48
