@@ -209,8 +209,8 @@ class QuestFeedForward(torch.nn.Module):
 
     norm_act8: the norm keeps its normalised input in 8 bits for the backward
     pass.  ``freeze()`` quantises the three weights once and switches to eval
-    mode, whose forwards then quantise activations only; training mode, loading
-    a state and moving the module drop the frozen operands.
+    mode, whose forwards then quantise activations only and carry no gradient;
+    training mode, loading a state and moving the module drop the frozen operands.
     """
 
     def __init__(self, features: int, width: int, block: int = 128, bits_x: int = 4, bits_w: int = 4,
@@ -259,14 +259,15 @@ class QuestFeedForward(torch.nn.Module):
         return super()._load_from_state_dict(*args, **kwargs)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y = x if self.norm is None else self.norm(x)
         if self.training or self._frozen is None:
+            y = x if self.norm is None else self.norm(x)
             h = quest_gated(y, self.gate, self.up, self.block, self.bits_x, self.bits_w, self.compute_dtype, self.act,
                             self.trust_x, self.trust_w)
             return self.down(h)
-        if y.shape[-1] != self.gate.shape[1]:
-            raise ValueError(f"the last axis of x has {y.shape[-1]} entries, the block {self.gate.shape[1]}")
-        with torch.no_grad():
+        if x.shape[-1] != self.gate.shape[1]:
+            raise ValueError(f"the last axis of x has {x.shape[-1]} entries, the block {self.gate.shape[1]}")
+        with torch.no_grad():  # (the norm too: with a gradient to follow it would keep its checkpoint)
+            y = x if self.norm is None else self.norm(x)
             flat = _dense(y.reshape(-1, y.shape[-1]))
             (go, gs), (uo, us) = self._frozen
             _, xs, _, xo = quantize_fwd_op(flat, self.block, self.bits_x, trust=self.trust_x)

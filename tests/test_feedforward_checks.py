@@ -265,3 +265,26 @@ def test_modules_on_the_cpu_refuse(lib):
         LayerNorm(128)(t(3, 100))
     with pytest.raises(ValueError, match="got"):
         quest_gated(t(3, 128), t(8, 256), t(8, 256))
+
+
+def test_frozen_block_keeps_nothing_for_a_backward_pass(monkeypatch):
+    """Frozen forwards carry no gradient, so their norm writes no checkpoint, also where gradients are enabled."""
+    from quantization_aware_amd import feedforward as ff_mod
+
+    asked = []
+
+    def norm_fwd(x, weight, bias, eps, act8=False):
+        asked.append(act8)
+        return x + weight + bias, t(x.shape[0]), t(x.shape[0]), pair(*x.shape) if act8 else None
+
+    monkeypatch.setattr(ff_mod, "layer_norm_fwd", norm_fwd)
+    monkeypatch.setattr(ff_mod, "quantize_fwd_op", lambda x, *a, **kw: (None, None, None, x))
+    monkeypatch.setattr(ff_mod, "gated_fwd", lambda x, *a, **kw: (x.repeat(1, 2), None, None))
+    ff = ff_mod.QuestFeedForward(128, 256)
+    ff.down.forward = lambda h: h[..., :128]
+    ff._frozen = [(None, None), (None, None)]
+    ff.eval()
+    x = t(3, 5, 128).requires_grad_()
+    y = ff(x)
+    assert asked == [False]
+    assert y.shape == (3, 5, 128) and not y.requires_grad
