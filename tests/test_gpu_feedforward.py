@@ -152,6 +152,33 @@ def test_gated_gradients(dev, n, k, m, block, bx, bw, act, cd):
     fo.check("h", h, hv * fo.f64(u2), np.abs(fo.f64(u2)) * hb + 2 * fo.U * np.abs(hv * fo.f64(u2)))
 
 
+@pytest.mark.parametrize("n,k,m,block,bx,bw,act", [
+    (64, 256, 96, 128, 4, 4, "silu"), (64, 256, 96, 128, 4, 4, "gelu"), (130, 512, 64, 256, 1, 1, "silu"),
+    (300, 384, 260, 64, 2, 4, "gelu"),
+])
+def test_gated_gradients_of_jointly_kept_weights(dev, n, k, m, block, bx, bw, act):
+    """Widths that are multiples of 4, whose two weights are rebuilt and masked as one: in fp32, entry by entry within
+    the counted roundings; in bf16, as a whole within 2^-8 of each gradient's norm.  (Three roundings to bf16 stand
+    behind an entry, of the product's left operand, its result and the output; each errs by 0.42 2^-8 of the value,
+    rms, and independently, together 0.74 2^-8; the bytes behind both sides are the same.  The fp32 bound is 64 half
+    steps, the same three and the products' sums of up to 520 terms.)"""
+    log(f"quest_gated closely {n}x{k}x{m} block {block} b={bx},{bw} {act}")
+    t = 1.3 if bx == 1 else 1.0, 1.3 if bw == 1 else 1.0
+    for cd in (torch.float32, torch.bfloat16):
+        x = rand((n, k), 11, cd, dev).requires_grad_()
+        gate = rand((m, k), 12, cd, dev, k ** -0.5).requires_grad_()
+        up = rand((m, k), 13, cd, dev, k ** -0.5).requires_grad_()
+        dh = rand((n, m), 14, cd, dev, 1e-2)
+        got = torch.autograd.grad(quest_gated(x, gate, up, block, bx, bw, cd, act), (x, gate, up), dh)
+        refs = reference_gradients(dev, x.detach(), gate.detach(), up.detach(), dh, block, bx, bw, act, *t, cd)
+        for name, g, (want, err) in zip(("dx", "dgate", "dup"), got, refs):
+            off = np.linalg.norm(fo.f64(g) - want) / np.linalg.norm(want)
+            log(f"{cd} {name}: {off * 256:.3g} 2^-8 of its norm")
+            if cd == torch.float32:
+                fo.check(name, g, want, err)
+            assert off <= 2.0 ** (-8 if cd == torch.bfloat16 else -18), (name, off)
+
+
 @pytest.mark.parametrize("needs", [(True, False, False), (False, True, False), (False, False, True), (False, True, True)])
 def test_gated_partial_gradients(dev, needs):
     log(f"gradients of {needs}")
