@@ -8,9 +8,12 @@ device.
 from __future__ import annotations
 
 import os
+import re
 
+import numpy as np
 import pytest
 import torch
+from scipy.special import erfcx
 
 import quantization_aware_amd as qa
 
@@ -288,3 +291,35 @@ def test_frozen_block_keeps_nothing_for_a_backward_pass(monkeypatch):
     y = ff(x)
     assert asked == [False]
     assert y.shape == (3, 5, 128) and not y.requires_grad
+
+
+def test_gelu_fit():
+    """normal_cdf's coefficients are the halved minimax fit of erfc(z) exp(z^2) by a polynomial of degree 8 in
+    t = 1 / (1 + 0.325 z), in relative error over 0 <= z <= 9.4: found here by exchange of its extrema in 64 bits,
+    and rounded to fp32."""
+    p, deg = 0.325, 8
+    src = open(os.path.join(os.path.dirname(qa.__file__), "csrc", "quest_gated.hip")).read()
+    body = src[src.index("float normal_cdf("):]
+    body = body[:body.index("const float q =")]
+    held = [float(a or b) for a, b in re.findall(r"float p = ([-0-9.e]+)f;|fmaf\(p, t, ([-0-9.e]+)f\)", body)]
+    scale = float(re.search(r"fmaf\(fabsf\(g\), ([0-9.]+)f, 1\.0f\)", body).group(1))
+    assert len(held) == deg + 1 and abs(scale - p / 2 ** 0.5) <= 2.0 ** -24 * scale * 2
+
+    def f(t):
+        return erfcx((1 / t - 1) / p)
+
+    lo = 1 / (1 + p * 9.4)
+    grid = np.linspace(lo, 1.0, 100001)
+    want = f(grid)
+    x = (lo + 1) / 2 + (1 - lo) / 2 * np.cos(np.pi * np.arange(deg + 1, -1, -1) / (deg + 1))
+    for _ in range(30):
+        rows = np.hstack([np.vander(x, deg + 1) / f(x)[:, None], ((-1.0) ** np.arange(deg + 2))[:, None]])
+        c = np.linalg.solve(rows, np.ones(deg + 2))[:-1]
+        r = np.polyval(c, grid) / want - 1
+        edges = np.flatnonzero(np.diff(np.sign(r))) + 1
+        ext = [s + np.argmax(np.abs(r[s:e])) for s, e in zip([0, *edges], [*edges, len(grid)])]
+        assert len(ext) == deg + 2
+        x = grid[ext]
+    top = np.abs(r).max()
+    assert 4.4e-8 < top < 4.6e-8 and np.abs(r[ext]).min() > 0.999 * top  # levelled: the best there is
+    assert (np.float32(held) == np.float32(c / 2)).all()
