@@ -453,9 +453,10 @@ size_t quest_sparse24_index_bytes(int64_t rows, int64_t cols);
 /*
  * The feed-forward half of a decoder layer around the quantised products:
  * activation checkpoints in 8 bits, layer norm and the gated product.  The
- * pages train Llama-family models with the quantiser on the inputs and weights
- * of every linear layer (pith.science review of QuEST, "What carries the
- * argument"); these are the operators between those products.  They take any
+ * pages put the quantiser on the inputs and weights of every linear layer
+ * (pith.science review of QuEST, "What carries the argument"); these are
+ * operators between such products.  The norm is the one that takes the mean
+ * out; a norm by the root mean square alone is not among them.  All take any
  * number of columns (no multiple is needed except where said).
  */
 
@@ -547,7 +548,9 @@ typedef enum {
  *   g = Q(X) Q(gate)^T,  u = Q(X) Q(up)^T  (n x m, each as quest_gemm's product),
  *   out = act(g) * u,
  * with one rounding, to out_dtype, after g and u (which are rounded as
- * quest_gemm's fp32 output).
+ * quest_gemm's fp32 output).  Clip scales may be infinite or NaN; the
+ * checkpoints are those that quest_act8_save gives of g and u, such blocks'
+ * among them.
  *   x, x_scale        operand of n rows and k columns, x_bits, as for quest_gemm
  *   gate, up          operands of m rows and k columns, w_bits, with their
  *                     clip scales gate_scale and up_scale

@@ -10,8 +10,8 @@
 // quest_act8.h; rows narrower than 8 go entry by entry); a workgroup takes a run
 // of consecutive blocks of the tensor, whatever rows they are of, so narrow rows
 // fill the waves as well as wide ones.  (16384 x 5631 bf16 is saved in 54.4 us and
-// read in 53.7, as 5632 columns are; with a branch for the last entries in 75.5
-// and 62.5.)
+// read in 53.7, with a branch for the last entries in 75.5 and 62.5; beside 5632
+// columns in one run 59.1 and 52.7 against 54.3 and 49.1.)
 #include "quest_act8.h"
 
 #include "quest_launch.h"

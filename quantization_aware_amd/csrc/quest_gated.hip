@@ -7,8 +7,8 @@
 // 8 bits of their checkpoints (quest_act8.h), which the training form writes.
 // The levels' products are quarter-integers whose sums stay below 2^22, so the
 // fp32 accumulation is exact in any order, and
-//   g[i][j] = acc[i][j] * ((sx[i] kx) * (sg[j] kw))
-// has three roundings and then the activation's.
+//   g[i][j] = acc[i][j] * ((sx[i] kx) * (sg[j] kw)),  k = 2 / (2^bits - 1),
+// has six roundings (two of them of kx and kw) and then the activation's.
 //
 // Kernel: a workgroup of 4 waves computes 64 kB rows x 64 kB columns of h.  The
 // two weight operands' blocks of 32 columns stand side by side in a stage of
@@ -18,11 +18,13 @@
 // kB = 2: two workgroups share a compute unit, each with two stages of 36 KB;
 // one's waits, activations and stores run beside the other's products.
 // 16384 x 2048 -> 5632 takes 258 us (2.93 PFLOP/s), 296 us with both
-// checkpoints; the products alone 212.  Bound by power: the clock is at 1.7 to
-// 1.9 of 2.4 GHz, the matrix cores 38% and LDS 50% busy, and work taken away
-// anywhere shows.  (256-row tiles of 8 waves, one workgroup a compute unit walking
-// its tiles, the next one's first stages requested before the stores: 252 and
-// 306 us.)
+// checkpoints; the products alone 212.  Bound by the bytes through LDS: a stage
+// moves 110 KB (36 written, 74 read) for 64 matrix instructions, and of 256 us
+// the loop without the loads into LDS saves 43, without the fragment reads 20,
+// without both 79, with half the matrix instructions 23.  Power sets the clock (1.85
+// to 1.96 of 2.4 GHz; matrix cores 34% and LDS 44% busy, 29% and 41% with checkpoints).
+// (256-row tiles of 8 waves, one workgroup a compute unit walking its tiles, the
+// next one's first stages requested before the stores: 252 and 306 us.)
 // kB = 1: four times the workgroups, for products whose larger tiles would
 // leave compute units without one; 256 rows take 10.5 us (15.4 with kB = 2).
 #include <type_traits>
@@ -35,8 +37,8 @@ namespace quest {
 namespace {
 
 // act(g) and act'(g).  kFast (silu): the hardware's reciprocal and exp2 (about
-// 2^-22 relative), for values that are rounded to bf16 next; fp32 results take
-// the full-precision functions.
+// 2^-22 relative), for values that are rounded to bf16 next; fp32 results of silu
+// take the full-precision functions.  gelu is normal_cdf's for both.
 template <bool kFast>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (kFast) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
@@ -524,8 +526,9 @@ __global__ void __launch_bounds__(64 * kFewWaves) quest_gated_few_kernel(const G
 // Backward: 8 columns a thread, a row a workgroup at a time.  kGroups: rows of a
 // whole number of groups of 8 (2), others of 8 columns and more (1: unaligned, the
 // last group ending with the row, see Group), narrower ones (0).  A streaming
-// kernel: 8.06 bytes an entry in bf16; 16384 x 5632 takes 141 to 154 us, 4.8 to 5.3
-// TB/s.
+// kernel: 8.06 bytes an entry in bf16; 16384 x 5632 takes 136 to 154 us, 4.8 to 5.5
+// TB/s (fp32 259).  Rows under some 2000 columns leave part of their workgroup idle:
+// 16384 x 1024 22 us, x 256 12, x 20 10.
 template <typename T, int kGroups, int kAct>
 __global__ void __launch_bounds__(256) quest_gated_bwd_kernel(const GatedBwdLaunch a) {
   const int cols = a.cols, blocks = (cols + kAct8Block - 1) / kAct8Block;

@@ -116,7 +116,7 @@ __device__ __forceinline__ bool inside(int t, int j, int i, int cols) {
 
 // Entries that are not the group's own as zeros.  Of a row's waves only the last and
 // those past it have any: the others pass by on a scalar branch (8000 x 5631 forward
-// 46 us, 57 with a select at every entry).
+// 46 us, 57 with a select at every entry, on one input; 52 where the inputs change).
 template <int TPR, bool kVec>
 __device__ __forceinline__ void own_only(int t, int j, int cols, float (&v)[8]) {
   if constexpr (TPR >= 64) {

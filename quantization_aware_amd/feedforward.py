@@ -13,7 +13,10 @@ trust masks of its operands, as QuestLinear does, and its two products, which
 the activation's gradient needs, in 8 bits (8.25 with the exponents, against
 16 in bf16 or 32): the gradients are those of act(g) u at the saved values
 (each within 2^-7 of the largest of its block of 32, 2^-6 where it is that
-largest).  Layer norm can keep its normalised input the same way (``act8``).
+largest).  Against gradients at the unrounded products, dx, dgate and dup of
+normal activations by normal weights (4096 x 2048 -> 5632) are off by 0.8 to 1.3%
+of their norm, where products kept in bf16 give 0.2%.  Layer norm can keep its
+normalised input the same way (``act8``).
 As in QuestLinear, the products of the backward pass are plain library GEMMs
 through torch on the dequantised operands; both weights' gradients are one of
 them and one trust backward, and so is the input's.
@@ -204,8 +207,8 @@ def quest_gated(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, block: in
 
 
 class QuestFeedForward(torch.nn.Module):
-    """Gated feed-forward block trained with QuEST quantisation: layer norm (optional), the gated product of
-    `width` columns, and a QuestLinear back to `features`.
+    """Gated feed-forward block trained with QuEST quantisation: layer norm (optional; with mean and bias), the
+    gated product of `width` columns, and a QuestLinear back to `features`.
 
     norm_act8: the norm keeps its normalised input in 8 bits for the backward
     pass.  ``freeze()`` quantises the three weights once and switches to eval
