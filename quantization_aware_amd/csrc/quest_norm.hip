@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) quest_norm_fwd_kernel(cons
     // those would be the larger error where the offset is small (16384 x 2048 bf16: mean
     // within 0.03 instead of 0.30 times 2^-24 of the spread, rms).
     off /= count;
-    if (fabsf(off) <= 0x1p-24f * __builtin_amdgcn_sqrtf(sq / count)) off = 0.0f;
+    if (fabsf(off) < 0x1p-24f * __builtin_amdgcn_sqrtf(sq / count)) off = 0.0f;  // (an infinity stays)
     const float mean = near + off;
     const float var = sq / count - off * off;
     const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);  // (NaN stays)

@@ -230,6 +230,19 @@ def test_statistics_of_bad_rows(dev, cols, bad):
         assert torch.isfinite(y[keep]).all() and torch.isfinite(rstd[keep]).all()
 
 
+@pytest.mark.parametrize("cols", [19, 700, 2048, 9001])
+def test_rows_whose_sum_overflows(dev, cols):
+    """Finite entries whose fp32 sum is none: no finite statistics either."""
+    log(f"overflow in {cols} columns")
+    for big in (3e38, -3e38):
+        x, _, w, b = inputs(5, cols, torch.float32, torch.float32, 9)
+        x[2] = big
+        y, mean, rstd, _ = run_fwd(dev, x, w, b)
+        assert torch.isnan(y[2]).all() and torch.isnan(rstd[2]) and not torch.isfinite(mean[2])
+        keep = [0, 1, 3, 4]
+        assert torch.isfinite(y[keep]).all() and torch.isfinite(rstd[keep]).all()
+
+
 def test_no_rows(dev):
     log("no rows")
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=dev)
