@@ -581,6 +581,44 @@ quest_status quest_gated_bwd(const void* dh, quest_dtype dtype, int64_t rows, in
                              const uint8_t* gate_exp, const int8_t* up_codes, const uint8_t* up_exp, quest_act act,
                              void* out, void* stream);
 
+/*
+ * Codes one a byte, the operand of the 8-bit integer products.  Everything as
+ * for quest_quantize_fwd_ex, for every b from 1 to 8, but
+ *   codes   rows * cols signed bytes, row-major: c = u - 2^(b-1), which stands
+ *           for (2 c + 1) s / (2^b - 1)
+ *   mask    or NULL (not written)
+ * A code next to a level's edge may differ from the packed one by a level (the
+ * two forwards round differently); here floor is taken of one rounded product.
+ */
+quest_status quest_quantize_fwd_i8(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, int block, int b,
+                                   double trust, int8_t* codes, float* scale, uint8_t* mask, void* stream);
+
+/* The values of such codes, (2 c + 1) s / (2^b - 1); sizes and types as for
+   quest_dequantize. */
+quest_status quest_dequantize_i8(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int b, void* out,
+                                 quest_dtype out_dtype, void* stream);
+
+/*
+ * Product of two such tensors in 8-bit integers, with a scale for each row of
+ * both (each token and each channel):
+ *   out[i][j] = D_a[i] D_b[j] sum_k (a[i][k] + 1/2)(b[j][k] + 1/2),
+ *   D = 2 s / (2^bits - 1).
+ * The sum is exact; it is rounded to fp32, multiplied by the product of the two
+ * steps and rounded to out_dtype.  Codes are taken as they are: those outside
+ * the range of a_bits or b_bits count with their value.
+ *   a, b          m x k and n x k signed bytes, row-major
+ *   a_bits, b_bits  1 .. 8, each its own
+ *   m, n, k       0 <= m <= 2^30, 0 <= n <= 2^20, k a positive multiple of 64 up
+ *                 to QUEST_MAX_COLS, and at most 2^23 - 1 tiles of 128 x 128
+ *                 (QUEST_EUNSUPPORTED)
+ *   out           m x n row-major elements of out_dtype
+ * All pointers 16-byte aligned (QUEST_EALIGN); out may not overlap another
+ * argument (QUEST_EINVAL).  a and b may be the same buffer.
+ */
+quest_status quest_gemm_i8(const int8_t* a, const float* a_scale, int64_t m, int a_bits, const int8_t* b,
+                           const float* b_scale, int64_t n, int b_bits, int64_t k, void* out, quest_dtype out_dtype,
+                           void* stream);
+
 /* Bytes of the packed codes: rows * cols * b / 8 (0 on invalid sizes). */
 size_t quest_codes_bytes(int64_t rows, int64_t cols, int b);
 

@@ -41,6 +41,9 @@ __all__ = [
     "layer_norm_bwd",
     "gated_fwd",
     "gated_bwd",
+    "quantize_fwd_i8",
+    "dequantize_i8",
+    "gemm_i8",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -82,6 +85,9 @@ EXPORTED_SYMBOLS = (
     "quest_layer_norm_bwd",
     "quest_gated_fwd",
     "quest_gated_bwd",
+    "quest_quantize_fwd_i8",
+    "quest_dequantize_i8",
+    "quest_gemm_i8",
     "quest_status_string",
 )
 
@@ -185,6 +191,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.quest_gated_fwd.restype = c_int
     lib.quest_gated_bwd.argtypes = [vp, c_int, i64, i64, vp, vp, vp, vp, c_int, vp, vp]
     lib.quest_gated_bwd.restype = c_int
+    lib.quest_quantize_fwd_i8.argtypes = [vp, c_int, i64, i64, c_int, c_int, ctypes.c_double, vp, vp, vp, vp]
+    lib.quest_quantize_fwd_i8.restype = c_int
+    lib.quest_dequantize_i8.argtypes = [vp, vp, i64, i64, c_int, vp, c_int, vp]
+    lib.quest_dequantize_i8.restype = c_int
+    lib.quest_gemm_i8.argtypes = [vp, vp, i64, c_int, vp, vp, i64, c_int, i64, vp, c_int, vp]
+    lib.quest_gemm_i8.restype = c_int
     lib.quest_status_string.argtypes = [c_int]
     lib.quest_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -952,4 +964,94 @@ def gated_bwd(dh: torch.Tensor, gate8, up8, act: str = "silu", out=None, stream=
         out = torch.empty(rows, 2 * cols, dtype=dh.dtype, device=dev)
     _launch("quest_gated_bwd", dev, dh.data_ptr(), code, rows, cols, gate8[0].data_ptr(), gate8[1].data_ptr(),
             up8[0].data_ptr(), up8[1].data_ptr(), act_code, out.data_ptr())
+    return out
+
+
+def quantize_fwd_i8(x: torch.Tensor, block: int, b: int, trust: float = 1.0, with_mask: bool = False, codes=None,
+                    scale=None, mask=None, stream=None):
+    """Forward quantisation to codes one a byte (quest_quantize_fwd_i8), the operand of gemm_i8 and moe_fwd.
+
+    Returns (codes, scale, mask or None): codes int8 (rows, cols), each the
+    packed code less 2^(b - 1); scale float32 (rows,); mask uint8 (rows,
+    cols / 8).  Allocated unless given; a given mask implies with_mask.
+    """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return quantize_fwd_i8(x, block, b, trust, with_mask, codes, scale, mask)
+    code = _matrix("x", x)
+    rows, cols = x.shape
+    dev = x.device
+    specs = (("x", x, x.dtype, None),)
+    if codes is not None:
+        specs += (("codes", codes, torch.int8, (rows, cols)),)
+    if scale is not None:
+        specs += (("scale", scale, torch.float32, (rows,)),)
+    if mask is not None:
+        specs += (("mask", mask, torch.uint8, (rows, cols // 8)),)
+    _check_tensors(dev, *specs)
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    if mask is None and with_mask:
+        mask = torch.empty(rows, cols // 8, dtype=torch.uint8, device=dev)
+    _launch("quest_quantize_fwd_i8", dev, x.data_ptr(), code, rows, cols, int(block), int(b), float(trust),
+            codes.data_ptr(), scale.data_ptr(), _ptr(mask))
+    return codes, scale, mask
+
+
+def _byte_codes(name: str, t) -> None:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D int8 tensor (rows x cols)")
+
+
+def dequantize_i8(codes: torch.Tensor, scale: torch.Tensor, b: int, out_dtype=torch.bfloat16, out=None,
+                  stream=None) -> torch.Tensor:
+    """Grid values (2 c + 1) s / (2^b - 1) of codes one a byte, in the Hadamard domain (quest_dequantize_i8)."""
+    if stream is not None:
+        with _on_stream(stream, codes):
+            return dequantize_i8(codes, scale, b, out_dtype, out)
+    _byte_codes("codes", codes)
+    rows, cols = codes.shape
+    dev = codes.device
+    specs = (("codes", codes, torch.int8, None), ("scale", scale, torch.float32, (rows,)))
+    if out is None:
+        code = _float_code(out_dtype)
+    else:
+        code = _matrix("out", out)
+        specs += (("out", out, out.dtype, (rows, cols)),)
+    _check_tensors(dev, *specs)
+    if out is None:
+        out = torch.empty(rows, cols, dtype=out_dtype, device=dev)
+    _launch("quest_dequantize_i8", dev, codes.data_ptr(), scale.data_ptr(), rows, cols, int(b), out.data_ptr(), code)
+    return out
+
+
+def gemm_i8(a: torch.Tensor, a_scale: torch.Tensor, a_bits: int, b: torch.Tensor, b_scale: torch.Tensor, b_bits: int,
+            out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """Product of two tensors of codes one a byte, in 8-bit integers (quest_gemm_i8).
+
+    a (m, k) and b (n, k) int8 with their clip scales (m,) and (n,), as
+    quantize_fwd_i8 gives them; returns (m, n) of out_dtype.
+    """
+    if stream is not None:
+        with _on_stream(stream, a):
+            return gemm_i8(a, a_scale, a_bits, b, b_scale, b_bits, out_dtype, out)
+    _byte_codes("a", a)
+    _byte_codes("b", b)
+    m, k = a.shape
+    n = b.shape[0]
+    dev = a.device
+    specs = (("a", a, torch.int8, None), ("a_scale", a_scale, torch.float32, (m,)), ("b", b, torch.int8, (n, k)),
+             ("b_scale", b_scale, torch.float32, (n,)))
+    if out is None:
+        code = _float_code(out_dtype)
+    else:
+        code = _matrix("out", out)
+        specs += (("out", out, out.dtype, (m, n)),)
+    _check_tensors(dev, *specs)
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype, device=dev)
+    _launch("quest_gemm_i8", dev, a.data_ptr(), a_scale.data_ptr(), m, int(a_bits), b.data_ptr(), b_scale.data_ptr(),
+            n, int(b_bits), k, out.data_ptr(), code)
     return out

@@ -218,6 +218,11 @@ constexpr int64_t kGemmMaxN = int64_t(1) << 20;
 constexpr int64_t kGemmMaxM = int64_t(1) << 30;
 constexpr int64_t kGemmMaxTiles = (int64_t(1) << 23) - 1;  // 256 x 256 output tiles
 
+// Bytes of rows x cols signed byte codes of a legal shape.
+size_t i8_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * static_cast<size_t>(cols); }
+
+float step_factor(int bits) { return static_cast<float>(2.0 / double((1 << bits) - 1)); }  // D over the clip scale
+
 }  // namespace
 
 extern "C" {
@@ -452,6 +457,84 @@ quest_status quest_gemm(const uint8_t* a, const float* a_scale, int64_t m, int a
   g.out = out;
   g.stream = static_cast<hipStream_t>(stream);
   return from_hip(quest::launch_gemm_e2m3(g, out_dtype == QUEST_BF16));
+}
+
+quest_status quest_quantize_fwd_i8(const void* x, quest_dtype x_dtype, int64_t rows, int64_t cols, int block, int b,
+                                   double trust, int8_t* codes, float* scale, uint8_t* mask, void* stream) {
+  const int lb = log2_block(block);
+  if (lb < 0 || b < 1 || b > kMaxBits) return QUEST_EUNSUPPORTED;
+  if (!dtype_ok(x_dtype) || !(trust >= 0.0) || !std::isfinite(trust)) return QUEST_EINVAL;
+  const quest_status sh = check_shape(rows, cols, block);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!x || !codes || !scale) return QUEST_EINVAL;
+  const Span spans[] = {{x, i8_bytes(rows, cols) * dtype_size(x_dtype), false},
+                        {codes, i8_bytes(rows, cols), true},
+                        {scale, static_cast<size_t>(rows) * sizeof(float), true},
+                        {mask, quest_mask_bytes(rows, cols), true}};
+  const quest_status st = check_spans(spans, 4);
+  if (st != QUEST_OK) return st;
+  quest::FwdLaunch a;
+  a.rows = rows;
+  a.cols = cols;
+  a.alpha = quest_fit_alpha(b);
+  a.trust = trust;
+  a.allow_mfma = false;
+  a.codes = reinterpret_cast<uint8_t*>(codes);
+  a.scale = scale;
+  a.mask = mask;
+  a.dq = nullptr;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_fwd_i8(x, x_dtype == QUEST_BF16, lb, b, a));
+}
+
+quest_status quest_dequantize_i8(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int b, void* out,
+                                 quest_dtype out_dtype, void* stream) {
+  if (b < 1 || b > kMaxBits) return QUEST_EUNSUPPORTED;
+  if (!dtype_ok(out_dtype)) return QUEST_EINVAL;
+  const quest_status sh = check_shape(rows, cols, 64);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!codes || !scale || !out) return QUEST_EINVAL;
+  const Span spans[] = {{codes, i8_bytes(rows, cols), false},
+                        {scale, static_cast<size_t>(rows) * sizeof(float), false},
+                        {out, i8_bytes(rows, cols) * dtype_size(out_dtype), true}};
+  const quest_status st = check_spans(spans, 3);
+  if (st != QUEST_OK) return st;
+  return from_hip(quest::launch_dequantize_i8(reinterpret_cast<const uint8_t*>(codes), scale, rows, cols, b, out,
+                                              out_dtype == QUEST_BF16, static_cast<hipStream_t>(stream)));
+}
+
+quest_status quest_gemm_i8(const int8_t* a, const float* a_scale, int64_t m, int a_bits, const int8_t* b,
+                           const float* b_scale, int64_t n, int b_bits, int64_t k, void* out, quest_dtype out_dtype,
+                           void* stream) {
+  if (a_bits < 1 || a_bits > kMaxBits || b_bits < 1 || b_bits > kMaxBits) return QUEST_EUNSUPPORTED;
+  if (!dtype_ok(out_dtype) || m < 0 || n < 0 || k <= 0) return QUEST_EINVAL;
+  if (k % 64 != 0 || k > QUEST_MAX_COLS || n > kGemmMaxN || m > kGemmMaxM) return QUEST_EUNSUPPORTED;
+  // 256 work-items per 128 x 128 tile: the launch's work-item count must fit 32 bits.
+  if (((m + 127) / 128) * ((n + 127) / 128) > kGemmMaxTiles) return QUEST_EUNSUPPORTED;
+  if (m == 0 || n == 0) return QUEST_OK;
+  if (!a || !a_scale || !b || !b_scale || !out) return QUEST_EINVAL;
+  const Span spans[] = {{a, i8_bytes(m, k), false},
+                        {a_scale, static_cast<size_t>(m) * sizeof(float), false},
+                        {b, i8_bytes(n, k), false},
+                        {b_scale, static_cast<size_t>(n) * sizeof(float), false},
+                        {out, i8_bytes(m, n) * dtype_size(out_dtype), true}};
+  const quest_status st = check_spans(spans, 5);
+  if (st != QUEST_OK) return st;
+  quest::GemmI8Launch g;
+  g.a = reinterpret_cast<const uint8_t*>(a);
+  g.sa = a_scale;
+  g.m = static_cast<int>(m);
+  g.b = reinterpret_cast<const uint8_t*>(b);
+  g.sb = b_scale;
+  g.n = static_cast<int>(n);
+  g.k = static_cast<int>(k);
+  g.ka = step_factor(a_bits);
+  g.kb = step_factor(b_bits);
+  g.out = out;
+  g.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_gemm_i8(g, out_dtype == QUEST_BF16));
 }
 
 double quest_fit_alpha_fp4(void) {

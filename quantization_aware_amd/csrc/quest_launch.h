@@ -209,4 +209,27 @@ struct GatedBwdLaunch {
 };
 hipError_t launch_gated_bwd(const GatedBwdLaunch& a, bool bf16);
 
+// The forward that writes its codes as signed bytes (a.codes; a.mask may be
+// null), and the values of such codes.  cols a multiple of 64, up to 32768.
+hipError_t launch_fwd_i8(const void* x, int x_is_bf16, int log_block, int bits, const FwdLaunch& a);
+hipError_t launch_dequantize_i8(const uint8_t* codes, const float* scale, int64_t rows, int64_t cols, int bits,
+                                void* out, int out_is_bf16, hipStream_t stream);
+
+// The product of two tensors of signed byte codes, already validated:
+// out (m x n, row-major) = D_a D_b * sum (a + 1/2)(b + 1/2) with D = scale * k*.
+struct GemmI8Launch {
+  const uint8_t* a;  // m x k
+  const float* sa;
+  int m;
+  const uint8_t* b;  // n x k
+  const float* sb;
+  int n;
+  int k;     // a multiple of 64, up to 32768
+  float ka;  // 2 / (L_a - 1)
+  float kb;
+  void* out;
+  hipStream_t stream;
+};
+hipError_t launch_gemm_i8(const GemmI8Launch& g, bool out_bf16);
+
 }  // namespace quest

@@ -28,15 +28,9 @@ from torch.autograd.function import once_differentiable
 
 from . import (ACTIVATIONS, dequantize, gated_bwd, gated_fwd, layer_norm_bwd, layer_norm_fwd, quantize_fwd_op,
                quantize_fwd_op_group, trust_bwd)
-from .linear import QuestLinear, default_trust
+from .linear import QuestLinear, _dense, default_trust
 
 __all__ = ["layer_norm", "LayerNorm", "quest_gated", "QuestFeedForward"]
-
-
-def _dense(t: torch.Tensor) -> torch.Tensor:
-    """t contiguous and on a 16-byte boundary (a view into a tensor may be neither), as the library takes it."""
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
 
 
 def _differentiates(*tensors) -> bool:

@@ -32,16 +32,25 @@ once into the FP6 matrix-core operand, each activation by
 quest_quantize_fwd_op, and the product is libquest's FP6 GEMM (quest_gemm):
 the 4-bit layer product whose speed the pages compare with BF16 (pith.science
 review, Figure 5 caption).
+
+``int8``: products in 8-bit integers, for 1 to 8 bits on the "int" grid (the
+pages train W8A8 models as well: pith.science review of QuEST, Figure 8
+caption).  Both operands are quantised to codes one a byte (quest_quantize_fwd_i8)
+and the forward product is quest_gemm_i8, with exact sums and one rounding to
+the compute dtype, where the default above 4 bits rounds both operands' values
+to the compute dtype first.  The backward rebuilds them (quest_dequantize_i8) for
+the same two gradient products.  ``freeze`` then keeps the weight's codes.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import (dequantize, gemm, quantize_fwd_ex, quantize_fwd_fp4, quantize_fwd_op, quantize_fwd_op_group,
-               quantize_fwd_sparse24, trust_bwd)
+from . import (dequantize, dequantize_i8, gemm, gemm_i8, quantize_fwd_ex, quantize_fwd_fp4, quantize_fwd_i8,
+               quantize_fwd_op, quantize_fwd_op_group, quantize_fwd_sparse24, trust_bwd)
 
-__all__ = ["QuestLinearFunction", "quest_linear", "quest_linear_operand", "QuestLinear", "default_trust",
-           "ONE_BIT_OUTER_TRUST", "GRIDS"]
+__all__ = ["QuestLinearFunction", "QuestLinearInt8Function", "quest_linear", "quest_linear_operand",
+           "quest_linear_int8", "QuestLinear", "default_trust", "ONE_BIT_OUTER_TRUST", "GRIDS"]
 
 
 ONE_BIT_OUTER_TRUST = 1.30  # pith.science review of QuEST, "Assumptions & free parameters" (s*)
@@ -181,19 +190,100 @@ class QuestLinearFunction(torch.autograd.Function):
         return g[:n].to(ctx.x_dtype), g[n:].to(ctx.w_dtype), None, None, None, None, None, None, None
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and on a 16-byte boundary (a view into a tensor may be neither), as the library takes it."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _product_dtype(compute_dtype):
+    """What a product writes: fp32 for fp32, bf16 for every other compute dtype (converted after it)."""
+    return torch.float32 if compute_dtype == torch.float32 else torch.bfloat16
+
+
+class QuestLinearInt8Function(torch.autograd.Function):
+    """y = Q(x) Q(w)^T for 2-D x (N x K) and w (M x K) in 8-bit integers, K a multiple of `block`."""
+
+    @staticmethod
+    def forward(ctx, x, w, block, bits_x, bits_w, compute_dtype, trust_x, trust_w, keep):
+        (n, k), m, dev = x.shape, w.shape[0], x.device
+        # As in QuestLinearFunction: with one bit width and n a multiple of 4 the codes, scales and
+        # masks of x and w are the rows of one tensor each, for one rebuild and one trust backward.
+        ctx.joint = keep and bits_x == bits_w and n % 4 == 0
+        outs = [{}, {}]
+        if ctx.joint:
+            codes = torch.empty((n + m, k), dtype=torch.int8, device=dev)
+            scale = torch.empty((n + m,), dtype=torch.float32, device=dev)
+            mask = torch.empty((n + m, k // 8), dtype=torch.uint8, device=dev)
+            outs = [dict(codes=codes[:n], scale=scale[:n], mask=mask[:n]),
+                    dict(codes=codes[n:], scale=scale[n:], mask=mask[n:])]
+        cx, sx, mx = quantize_fwd_i8(x, block, bits_x, trust_x, with_mask=keep, **outs[0])
+        cw, sw, mw = quantize_fwd_i8(w, block, bits_w, trust_w, with_mask=keep, **outs[1])
+        if ctx.joint:
+            ctx.save_for_backward(codes, scale, mask)
+        elif keep:
+            ctx.save_for_backward(cx, sx, mx, cw, sw, mw)
+        ctx.dims = (n, m, k, block, bits_x, bits_w, compute_dtype)
+        ctx.dtypes = (x.dtype, w.dtype)
+        return gemm_i8(cx, sx, bits_x, cw, sw, bits_w, out_dtype=_product_dtype(compute_dtype)).to(compute_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        n, m, k, block, bits_x, bits_w, compute_dtype = ctx.dims
+        need_x, need_w = ctx.needs_input_grad[:2]
+        if ctx.joint:
+            codes, scale, mask = ctx.saved_tensors
+            cx, sx, mx, cw, sw, mw = codes[:n], scale[:n], mask[:n], codes[n:], scale[n:], mask[n:]
+        else:
+            cx, sx, mx, cw, sw, mw = ctx.saved_tensors
+        dtype = _product_dtype(compute_dtype)
+        dy = dy.to(dtype).contiguous()
+        if ctx.joint and need_x and need_w:
+            q = dequantize_i8(codes, scale, bits_x, out_dtype=dtype)
+            g = torch.empty((n + m, k), dtype=dtype, device=dy.device)
+            torch.mm(dy.t(), q[:n], out=g[n:])  # the weight's first, as in QuestLinearFunction
+            torch.mm(dy, q[n:], out=g[:n])
+            trust_bwd(g, mask, block, out=g)
+            return g[:n].to(ctx.dtypes[0]), g[n:].to(ctx.dtypes[1]), *(None,) * 7
+        dx = dw = None
+        if need_w:
+            g = torch.mm(dy.t(), dequantize_i8(cx, sx, bits_x, out_dtype=dtype))
+            dw = trust_bwd(g, mw, block, out=g).to(ctx.dtypes[1])
+        if need_x:
+            g = torch.mm(dy, dequantize_i8(cw, sw, bits_w, out_dtype=dtype))
+            dx = trust_bwd(g, mx, block, out=g).to(ctx.dtypes[0])
+        return dx, dw, *(None,) * 7
+
+
+def _check_int8(grid: str, in_features: int, bits_x: int, bits_w: int) -> None:
+    if grid != "int" or not (1 <= bits_x <= 8 and 1 <= bits_w <= 8) or in_features > 32768:
+        raise ValueError("products in 8-bit integers need the int grid, 1 to 8 bits and at most 32768 in_features: got "
+                         f"{grid!r}, {bits_x} and {bits_w} bits, {in_features} in_features")
+
+
 def quest_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, block: int = 128,
                  bits_x: int = 4, bits_w: int = 4, compute_dtype=torch.bfloat16, trust_x: float | None = None,
-                 trust_w: float | None = None, grid: str = "int") -> torch.Tensor:
+                 trust_w: float | None = None, grid: str = "int", int8: bool = False) -> torch.Tensor:
     """QuEST linear map of x (..., K) by w (M, K); leading axes of x are flattened.
 
     trust_x / trust_w: outer trust factors; by default 1.30 for 1-bit operands
     of the "int" grid (the factor the pages tune for their 1-bit runs) and 1
-    otherwise.  grid: "int", "fp4" or "sparse24".
+    otherwise.  grid: "int", "fp4" or "sparse24".  int8: the product in 8-bit
+    integers (1 to 8 bits, the "int" grid).
     """
     _check_grid(grid)
     trust_x = (default_trust(bits_x) if grid == "int" else 1.0) if trust_x is None else trust_x
     trust_w = (default_trust(bits_w) if grid == "int" else 1.0) if trust_w is None else trust_w
     lead = x.shape[:-1]
+    if int8:
+        _check_int8(grid, x.shape[-1], bits_x, bits_w)
+        x2, w2 = _dense(x.reshape(-1, x.shape[-1])), _dense(w)
+        keep = torch.is_grad_enabled() and (x2.requires_grad or w2.requires_grad)
+        y = QuestLinearInt8Function.apply(x2, w2, block, bits_x, bits_w, compute_dtype, trust_x, trust_w, keep)
+        if bias is not None:
+            y = y + bias.to(y.dtype)
+        return y.reshape(*lead, w.shape[0])
     x2 = x.reshape(-1, x.shape[-1]).contiguous()
     y = QuestLinearFunction.apply(x2, w.contiguous(), block, bits_x, bits_w, compute_dtype, trust_x, trust_w, grid)
     if bias is not None:
@@ -221,16 +311,35 @@ def quest_linear_operand(x: torch.Tensor, w_operand: torch.Tensor, w_scale: torc
     return y.reshape(*lead, out_features)
 
 
+def quest_linear_int8(x: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Tensor, bits_w: int,
+                      bias: torch.Tensor | None = None, block: int = 128, bits_x: int = 8,
+                      out_dtype=torch.bfloat16) -> torch.Tensor:
+    """Inference product Q(x) Q(w)^T (+ bias) in 8-bit integers, with w already quantised.
+
+    x (..., K) bf16 or fp32; w_codes (M, K) int8 and w_scale (M,) as returned
+    by quantize_fwd_i8 at bits_w.  No gradient flows.
+    """
+    x2 = _dense(x.detach().reshape(-1, x.shape[-1]))
+    cx, sx, _ = quantize_fwd_i8(x2, block, bits_x)
+    y = gemm_i8(cx, sx, bits_x, w_codes, w_scale, bits_w, out_dtype=out_dtype)
+    if bias is not None:
+        y = y + bias.to(y.dtype)
+    return y.reshape(*x.shape[:-1], w_codes.shape[0])
+
+
 class QuestLinear(torch.nn.Module):
-    """Drop-in linear layer trained with QuEST quantisation of weights and activations."""
+    """Drop-in linear layer trained with QuEST quantisation of weights and activations (int8: as in quest_linear)."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, block: int = 128, bits_x: int = 4,
                  bits_w: int = 4, compute_dtype=torch.bfloat16, trust_x: float | None = None,
-                 trust_w: float | None = None, grid: str = "int", device=None, dtype=None):
+                 trust_w: float | None = None, grid: str = "int", device=None, dtype=None, int8: bool = False):
         super().__init__()
         if in_features % block:
             raise ValueError(f"in_features ({in_features}) must be a multiple of the Hadamard block ({block})")
         _check_grid(grid)
+        if int8:
+            _check_int8(grid, in_features, bits_x, bits_w)
+        self.int8 = int8
         self.block, self.bits_x, self.bits_w, self.compute_dtype = block, bits_x, bits_w, compute_dtype
         self.grid = grid
         self.trust_x = (default_trust(bits_x) if grid == "int" else 1.0) if trust_x is None else trust_x
@@ -243,7 +352,14 @@ class QuestLinear(torch.nn.Module):
     def freeze(self) -> "QuestLinear":
         """Quantise the weight once into the FP6 operand and switch to eval mode; eval-mode
         forwards then run the matrix-core product.  Needs bits_x, bits_w <= 4 and
-        in_features a multiple of 128, on the "int" grid; training mode (``train()``) drops the operand."""
+        in_features a multiple of 128, on the "int" grid; training mode (``train()``) drops the operand.
+        With int8 the weight's codes are kept instead, and the product is the one in 8-bit integers; loading a
+        state and moving the module drop them as well."""
+        if self.int8:
+            with torch.no_grad():
+                self._w_operand, self._w_scale, _ = quantize_fwd_i8(_dense(self.weight.detach()), self.block,
+                                                                    self.bits_w)
+            return self.eval()
         if self.grid != "int" or max(self.bits_x, self.bits_w) > 4 or self.weight.shape[1] % 128:
             raise ValueError("the FP6 product needs the int grid, bits <= 4 and in_features a multiple of 128")
         with torch.no_grad():
@@ -256,10 +372,23 @@ class QuestLinear(torch.nn.Module):
             self._w_operand = self._w_scale = None
         return super().train(mode)
 
+    def _apply(self, *args, **kwargs):
+        if self.int8:
+            self._w_operand = self._w_scale = None
+        return super()._apply(*args, **kwargs)
+
+    def _load_from_state_dict(self, *args, **kwargs):
+        if self.int8:
+            self._w_operand = self._w_scale = None
+        return super()._load_from_state_dict(*args, **kwargs)
+
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if not self.training and self._w_operand is not None:
-            out_dtype = torch.float32 if self.compute_dtype == torch.float32 else torch.bfloat16
+            out_dtype = _product_dtype(self.compute_dtype)
+            if self.int8:
+                return quest_linear_int8(x, self._w_operand, self._w_scale, self.bits_w, self.bias, self.block,
+                                         self.bits_x, out_dtype)
             return quest_linear_operand(x, self._w_operand, self._w_scale, self.weight.shape[0], self.bits_w,
                                         self.bias, self.block, self.bits_x, out_dtype)
         return quest_linear(x, self.weight, self.bias, self.block, self.bits_x, self.bits_w, self.compute_dtype,
-                            self.trust_x, self.trust_w, self.grid)
+                            self.trust_x, self.trust_w, self.grid, self.int8)
