@@ -619,6 +619,44 @@ quest_status quest_gemm_i8(const int8_t* a, const float* a_scale, int64_t m, int
                            const float* b_scale, int64_t n, int b_bits, int64_t k, void* out, quest_dtype out_dtype,
                            void* stream);
 
+/*
+ * A whole mixture-of-experts layer for a few tokens, on quantised weights:
+ *   out_t = sum over the experts e that token t takes of
+ *           p_te Q(h_te) Q(down_e)^T,
+ *   h_te = act(Q(x_t) Q(gate_e)^T) * (Q(x_t) Q(up_e)^T).
+ * A token takes the top_k experts with the largest logits, of equal ones the
+ * lowest index.  p is the softmax over their logits, or with over_all over all of
+ * the token's.  An expert with a logit of -infinity is never taken; a token that
+ * takes none gives zeros, one with a NaN or +infinity among its logits NaN.
+ * Products are sums of whole numbers, scaled in fp32; h is kept in fp32 and
+ * quantised to h_bits as by quest_quantize_fwd_i8, with `block`; the products of
+ * a token's experts are added in fp32 in the order of their logits, and rounded
+ * once to out_dtype.
+ *   x, x_scale      n x k codes one a byte (quest_quantize_fwd_i8), x_bits
+ *   logits          n x experts elements of logits_dtype
+ *   gate, up        experts x m x k codes, their scales gate_scale and up_scale
+ *                   experts x m floats
+ *   down            experts x k x m codes, down_scale experts x k floats
+ *   w_bits          of all three; w_packed 0: codes one a byte, 1: the packed
+ *                   codes of quest_quantize_fwd, for w_bits 4
+ *   n               0 .. 64;  experts 1 .. 256;  top_k 1 .. 32, at most experts
+ *   k               a positive multiple of 64 up to QUEST_MAX_COLS
+ *   m               a positive multiple of block (64, 128 or 256) up to 8192
+ *   out             n x k elements of out_dtype
+ *   workspace       device, quest_moe_workspace_bytes(n, top_k, k, m) bytes (0 on
+ *                   invalid sizes), need not be set and is written.  Calls that
+ *                   can run at the same time need one each.
+ * The result does not depend on timing: every sum has a fixed order.  All
+ * pointers 16-byte aligned (QUEST_EALIGN); out and workspace may not overlap
+ * another argument (QUEST_EINVAL).
+ */
+size_t quest_moe_workspace_bytes(int64_t n, int64_t top_k, int64_t k, int64_t m);
+quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int x_bits, const void* logits,
+                           quest_dtype logits_dtype, int64_t experts, int64_t top_k, int over_all, const void* gate,
+                           const float* gate_scale, const void* up, const float* up_scale, const void* down,
+                           const float* down_scale, int w_bits, int w_packed, int64_t k, int64_t m, int block,
+                           int h_bits, quest_act act, void* out, quest_dtype out_dtype, void* workspace, void* stream);
+
 /* Bytes of the packed codes: rows * cols * b / 8 (0 on invalid sizes). */
 size_t quest_codes_bytes(int64_t rows, int64_t cols, int b);
 

@@ -44,6 +44,7 @@ __all__ = [
     "quantize_fwd_i8",
     "dequantize_i8",
     "gemm_i8",
+    "moe_fwd",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -88,6 +89,8 @@ EXPORTED_SYMBOLS = (
     "quest_quantize_fwd_i8",
     "quest_dequantize_i8",
     "quest_gemm_i8",
+    "quest_moe_workspace_bytes",
+    "quest_moe_fwd",
     "quest_status_string",
 )
 
@@ -197,6 +200,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.quest_dequantize_i8.restype = c_int
     lib.quest_gemm_i8.argtypes = [vp, vp, i64, c_int, vp, vp, i64, c_int, i64, vp, c_int, vp]
     lib.quest_gemm_i8.restype = c_int
+    lib.quest_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.quest_moe_workspace_bytes.restype = ctypes.c_size_t
+    lib.quest_moe_fwd.argtypes = [vp, vp, i64, c_int, vp, c_int, i64, i64, c_int, vp, vp, vp, vp, vp, vp, c_int, c_int,
+                                  i64, i64, c_int, c_int, c_int, vp, c_int, vp, vp]
+    lib.quest_moe_fwd.restype = c_int
     lib.quest_status_string.argtypes = [c_int]
     lib.quest_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -1054,4 +1062,61 @@ def gemm_i8(a: torch.Tensor, a_scale: torch.Tensor, a_bits: int, b: torch.Tensor
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     _launch("quest_gemm_i8", dev, a.data_ptr(), a_scale.data_ptr(), m, int(a_bits), b.data_ptr(), b_scale.data_ptr(),
             n, int(b_bits), k, out.data_ptr(), code)
+    return out
+
+
+MOE_MAX_TOKENS = 64  # quest_moe_fwd
+
+
+def moe_fwd(x: torch.Tensor, x_scale: torch.Tensor, x_bits: int, logits: torch.Tensor, gate: torch.Tensor,
+            gate_scale: torch.Tensor, up: torch.Tensor, up_scale: torch.Tensor, down: torch.Tensor,
+            down_scale: torch.Tensor, w_bits: int, top_k: int, block: int = 128, h_bits: int | None = None,
+            act: str = "silu", over_all: bool = False, out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for up to 64 tokens (quest_moe_fwd); returns (n, k) of out_dtype.
+
+    x (n, k) int8 codes and x_scale (n,), as quantize_fwd_i8 gives them; logits
+    (n, experts) float32 or bfloat16.  Weights gate and up (experts, m, k) and
+    down (experts, k, m) as int8 codes, or, at 4 bits, uint8 packed codes (last
+    axis halved) as quantize_fwd gives them; scales (experts, m) and
+    (experts, k).  h_bits defaults to x_bits.  over_all: weights from the
+    softmax over all logits, not over the chosen ones.
+    """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return moe_fwd(x, x_scale, x_bits, logits, gate, gate_scale, up, up_scale, down, down_scale, w_bits, top_k,
+                           block, h_bits, act, over_all, out_dtype, out)
+    _byte_codes("x", x)
+    logits_code = _matrix("logits", logits)
+    act_code = _act_code(act)
+    n, k = x.shape
+    experts, top_k = logits.shape[1], int(top_k)
+    if not 1 <= top_k <= experts:
+        raise ValueError(f"top_k is 1 to the number of experts ({experts}), not {top_k}")
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 3 or gate.dtype not in (torch.int8, torch.uint8):
+        raise ValueError("gate must be a 3-D int8 (codes) or uint8 (packed 4-bit codes) tensor")
+    packed = gate.dtype == torch.uint8
+    if packed and w_bits != 4:
+        raise ValueError(f"packed codes (uint8) are of 4 bits, not {w_bits}")
+    m, per = gate.shape[1], 2 if packed else 1
+    dev = x.device
+    wide, tall = (experts, m, k // per), (experts, k, m // per)
+    specs = (("x", x, torch.int8, None), ("x_scale", x_scale, torch.float32, (n,)),
+             ("logits", logits, logits.dtype, (n, experts)), ("gate", gate, gate.dtype, wide),
+             ("gate_scale", gate_scale, torch.float32, (experts, m)), ("up", up, gate.dtype, wide),
+             ("up_scale", up_scale, torch.float32, (experts, m)), ("down", down, gate.dtype, tall),
+             ("down_scale", down_scale, torch.float32, (experts, k)))
+    if out is None:
+        code = _float_code(out_dtype)
+    else:
+        code = _matrix("out", out)
+        specs += (("out", out, out.dtype, (n, k)),)
+    _check_tensors(dev, *specs)
+    if out is None:
+        out = torch.empty(n, k, dtype=out_dtype, device=dev)
+    need = 4 * min(n, MOE_MAX_TOKENS) * top_k * (k + m)  # quest_moe_workspace_bytes
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _launch("quest_moe_fwd", dev, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), logits.data_ptr(), logits_code,
+            experts, top_k, int(over_all), gate.data_ptr(), gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(),
+            down.data_ptr(), down_scale.data_ptr(), int(w_bits), int(packed), k, m, int(block),
+            int(x_bits if h_bits is None else h_bits), act_code, out.data_ptr(), code, ws.data_ptr())
     return out

@@ -537,6 +537,81 @@ quest_status quest_gemm_i8(const int8_t* a, const float* a_scale, int64_t m, int
   return from_hip(quest::launch_gemm_i8(g, out_dtype == QUEST_BF16));
 }
 
+size_t quest_moe_workspace_bytes(int64_t n, int64_t top_k, int64_t k, int64_t m) {
+  if (n < 0 || n > quest::kMoeMaxTokens || top_k < 1 || top_k > quest::kMoeMaxTop || k <= 0 || k > QUEST_MAX_COLS ||
+      m <= 0 || m > quest::kMoeMaxWidth)
+    return 0;
+  return static_cast<size_t>(n * top_k) * static_cast<size_t>(k + m) * sizeof(float);
+}
+
+quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int x_bits, const void* logits,
+                           quest_dtype logits_dtype, int64_t experts, int64_t top_k, int over_all, const void* gate,
+                           const float* gate_scale, const void* up, const float* up_scale, const void* down,
+                           const float* down_scale, int w_bits, int w_packed, int64_t k, int64_t m, int block,
+                           int h_bits, quest_act act, void* out, quest_dtype out_dtype, void* workspace, void* stream) {
+  const int lb = log2_block(block);
+  if (lb < 0 || x_bits < 1 || x_bits > kMaxBits || w_bits < 1 || w_bits > kMaxBits || h_bits < 1 || h_bits > kMaxBits ||
+      (w_packed && w_bits != 4))
+    return QUEST_EUNSUPPORTED;
+  if (!dtype_ok(logits_dtype) || !dtype_ok(out_dtype) || !act_ok(act) || n < 0 || experts <= 0 || top_k <= 0 ||
+      top_k > experts || k <= 0 || m <= 0 || m % block != 0)
+    return QUEST_EINVAL;
+  if (n > quest::kMoeMaxTokens || experts > quest::kMoeMaxExperts || top_k > quest::kMoeMaxTop || k % 64 != 0 ||
+      k > QUEST_MAX_COLS || m > quest::kMoeMaxWidth)
+    return QUEST_EUNSUPPORTED;
+  if (n == 0) return QUEST_OK;
+  if (!x || !x_scale || !logits || !gate || !gate_scale || !up || !up_scale || !down || !down_scale || !out ||
+      !workspace)
+    return QUEST_EINVAL;
+  const size_t weights = i8_bytes(experts * m, k) / (w_packed ? 2 : 1);
+  const size_t per_m = static_cast<size_t>(experts * m) * sizeof(float);
+  const Span spans[] = {{x, i8_bytes(n, k), false},
+                        {x_scale, static_cast<size_t>(n) * sizeof(float), false},
+                        {logits, static_cast<size_t>(n * experts) * dtype_size(logits_dtype), false},
+                        {gate, weights, false},
+                        {gate_scale, per_m, false},
+                        {up, weights, false},
+                        {up_scale, per_m, false},
+                        {down, weights, false},
+                        {down_scale, static_cast<size_t>(experts * k) * sizeof(float), false},
+                        {out, i8_bytes(n, k) * dtype_size(out_dtype), true},
+                        {workspace, quest_moe_workspace_bytes(n, top_k, k, m), true}};
+  const quest_status st = check_spans(spans, 11);
+  if (st != QUEST_OK) return st;
+  quest::MoeLaunch a;
+  a.x = reinterpret_cast<const uint8_t*>(x);
+  a.sx = x_scale;
+  a.n = static_cast<int>(n);
+  a.logits = logits;
+  a.experts = static_cast<int>(experts);
+  a.top = static_cast<int>(top_k);
+  a.over_all = over_all != 0;
+  a.slots = static_cast<int>(experts < n * top_k ? experts : n * top_k);
+  a.gate = static_cast<const uint8_t*>(gate);
+  a.sg = gate_scale;
+  a.up = static_cast<const uint8_t*>(up);
+  a.su = up_scale;
+  a.down = static_cast<const uint8_t*>(down);
+  a.sd = down_scale;
+  a.k = static_cast<int>(k);
+  a.m = static_cast<int>(m);
+  a.block = block;
+  a.act = static_cast<int>(act);
+  a.kx = step_factor(x_bits);
+  a.kw = step_factor(w_bits);
+  a.kh = step_factor(h_bits);
+  const double alpha = quest_fit_alpha(h_bits), levels = double(1 << h_bits);
+  a.halpha = static_cast<float>(alpha);
+  a.hkk = static_cast<float>((levels - 1.0) / (2.0 * alpha * std::sqrt(double(block))));
+  a.h_half = static_cast<float>(levels / 2.0);
+  a.inv_m = static_cast<float>(1.0 / double(m));
+  a.h = static_cast<float*>(workspace);
+  a.y = a.h + n * top_k * m;
+  a.out = out;
+  a.stream = static_cast<hipStream_t>(stream);
+  return from_hip(quest::launch_moe(a, w_packed != 0, logits_dtype == QUEST_BF16, out_dtype == QUEST_BF16));
+}
+
 double quest_fit_alpha_fp4(void) {
   std::call_once(g_alpha_once, fill_alpha_table);
   return g_alpha_fp4;

@@ -30,19 +30,6 @@ __device__ __forceinline__ int sum4(v4i f, int acc) {
   return acc;
 }
 
-// 16 bytes of LDS to a row's `left` last elements at any multiple of T's size:
-// in one store, or the row's last few one by one.
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* dst, const uint8_t* src, int left) {
-  typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(1)));
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-  if (left >= kPer) {
-    *reinterpret_cast<u32x4_u*>(dst) = *reinterpret_cast<const u32x4*>(src);
-  } else {
-    for (int e = 0; e < left; ++e) dst[e] = reinterpret_cast<const T*>(src)[e];
-  }
-}
-
 // A workgroup of WM x WN waves computes 32 IB WM rows by 32 JB WN columns.
 // Both operands are row-major bytes; a stage is 64 bytes of k of every row, four
 // 16-byte chunks a row, straight from memory into LDS.  Chunk c of row r lies in

@@ -232,4 +232,39 @@ struct GemmI8Launch {
 };
 hipError_t launch_gemm_i8(const GemmI8Launch& g, bool out_bf16);
 
+// A mixture-of-experts layer for a few tokens, already validated.  Weights are
+// signed byte codes (experts x m x k, down experts x k x m), or packed 4-bit ones.
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTop = 32, kMoeMaxWidth = 8192;
+struct MoeLaunch {
+  const uint8_t* x;  // n x k codes
+  const float* sx;
+  int n;
+  const void* logits;  // n x experts
+  int experts;
+  int top;
+  bool over_all;  // softmax over all logits, not the chosen ones
+  int slots;      // min(experts, n * top)
+  const uint8_t* gate;
+  const float* sg;
+  const uint8_t* up;
+  const float* su;
+  const uint8_t* down;
+  const float* sd;
+  int k;  // a multiple of 64
+  int m;  // a multiple of block
+  int block;
+  int act;  // 0 silu, 1 gelu
+  float kx, kw, kh;           // 2 / (L - 1) of x, the weights and h
+  float halpha, hkk, h_half;  // of h's quantisation: clip scale over RMS, codes over transformed values, L / 2
+  float inv_m;
+  float* h;  // workspace: n * top rows of m
+  float* y;  // workspace: n * top rows of k
+  void* out;
+  hipStream_t stream;
+};
+// Bytes between two rows of quantised h in LDS: whole chunks of 128 columns, and 16
+// more, so that 16 rows' 16 bytes at one column lie in different banks.
+constexpr int moe_code_pitch(int m) { return ((m + 127) & ~127) + 16; }
+hipError_t launch_moe(const MoeLaunch& a, bool packed, bool logits_bf16, bool out_bf16);
+
 }  // namespace quest
