@@ -541,7 +541,8 @@ size_t quest_moe_workspace_bytes(int64_t n, int64_t top_k, int64_t k, int64_t m)
   if (n < 0 || n > quest::kMoeMaxTokens || top_k < 1 || top_k > quest::kMoeMaxTop || k <= 0 || k > QUEST_MAX_COLS ||
       m <= 0 || m > quest::kMoeMaxWidth)
     return 0;
-  return static_cast<size_t>(n * top_k) * static_cast<size_t>(k + m) * sizeof(float);
+  // a row for each token and rank: h and the products in fp32, h's codes and clip scale
+  return static_cast<size_t>(n * top_k) * static_cast<size_t>(4 * k + 5 * m + 16);
 }
 
 quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int x_bits, const void* logits,
@@ -583,6 +584,7 @@ quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int
   a.sx = x_scale;
   a.n = static_cast<int>(n);
   a.logits = logits;
+  a.logits_bf16 = logits_dtype == QUEST_BF16;
   a.experts = static_cast<int>(experts);
   a.top = static_cast<int>(top_k);
   a.over_all = over_all != 0;
@@ -595,21 +597,21 @@ quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int
   a.sd = down_scale;
   a.k = static_cast<int>(k);
   a.m = static_cast<int>(m);
-  a.block = block;
+  a.log_block = lb;
+  a.h_bits = h_bits;
+  a.halpha = quest_fit_alpha(h_bits);
   a.act = static_cast<int>(act);
   a.kx = step_factor(x_bits);
   a.kw = step_factor(w_bits);
   a.kh = step_factor(h_bits);
-  const double alpha = quest_fit_alpha(h_bits), levels = double(1 << h_bits);
-  a.halpha = static_cast<float>(alpha);
-  a.hkk = static_cast<float>((levels - 1.0) / (2.0 * alpha * std::sqrt(double(block))));
-  a.h_half = static_cast<float>(levels / 2.0);
-  a.inv_m = static_cast<float>(1.0 / double(m));
+  const int64_t rows = n * top_k;
   a.h = static_cast<float*>(workspace);
-  a.y = a.h + n * top_k * m;
+  a.y = a.h + rows * m;
+  a.hc = reinterpret_cast<uint8_t*>(a.y + rows * k);
+  a.hs = reinterpret_cast<float*>(a.hc + rows * m);
   a.out = out;
   a.stream = static_cast<hipStream_t>(stream);
-  return from_hip(quest::launch_moe(a, w_packed != 0, logits_dtype == QUEST_BF16, out_dtype == QUEST_BF16));
+  return from_hip(quest::launch_moe(a, w_packed != 0, out_dtype == QUEST_BF16));
 }
 
 double quest_fit_alpha_fp4(void) {

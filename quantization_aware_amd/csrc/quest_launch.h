@@ -240,6 +240,7 @@ struct MoeLaunch {
   const float* sx;
   int n;
   const void* logits;  // n x experts
+  bool logits_bf16;
   int experts;
   int top;
   bool over_all;  // softmax over all logits, not the chosen ones
@@ -252,19 +253,18 @@ struct MoeLaunch {
   const float* sd;
   int k;  // a multiple of 64
   int m;  // a multiple of block
-  int block;
-  int act;  // 0 silu, 1 gelu
-  float kx, kw, kh;           // 2 / (L - 1) of x, the weights and h
-  float halpha, hkk, h_half;  // of h's quantisation: clip scale over RMS, codes over transformed values, L / 2
-  float inv_m;
-  float* h;  // workspace: n * top rows of m
-  float* y;  // workspace: n * top rows of k
+  int log_block, h_bits;  // of h's quantisation
+  double halpha;          // its clip scale over the RMS
+  int act;                // 0 silu, 1 gelu
+  float kx, kw, kh;       // 2 / (L - 1) of x, the weights and h
+  // workspace, n * top rows each:
+  float* h;     // of m
+  float* y;     // of k
+  uint8_t* hc;  // of m: h's codes
+  float* hs;    // and their clip scales
   void* out;
   hipStream_t stream;
 };
-// Bytes between two rows of quantised h in LDS: whole chunks of 128 columns, and 16
-// more, so that 16 rows' 16 bytes at one column lie in different banks.
-constexpr int moe_code_pitch(int m) { return ((m + 127) & ~127) + 16; }
-hipError_t launch_moe(const MoeLaunch& a, bool packed, bool logits_bf16, bool out_bf16);
+hipError_t launch_moe(const MoeLaunch& a, bool packed, bool out_bf16);
 
 }  // namespace quest
