@@ -235,6 +235,11 @@ hipError_t launch_gemm_i8(const GemmI8Launch& g, bool out_bf16);
 // A mixture-of-experts layer for a few tokens, already validated.  Weights are
 // signed byte codes (experts x m x k, down experts x k x m), or packed 4-bit ones.
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTop = 32, kMoeMaxWidth = 8192;
+struct MoeSlot {  // a chosen expert and its tokens: token | rank of the expert among the token's << 8
+  int expert, count;
+  uint16_t entry[kMoeMaxTokens];
+  int unused[2];  // (to a multiple of 16 bytes)
+};
 struct MoeLaunch {
   const uint8_t* x;  // n x k codes
   const float* sx;
@@ -262,6 +267,10 @@ struct MoeLaunch {
   float* y;     // of k
   uint8_t* hc;  // of m: h's codes
   float* hs;    // and their clip scales
+  float* weight;  // of the expert of each rank
+  int* found;     // experts of each of the n tokens, or -1 for one whose output is NaN
+  MoeSlot* slot;  // at most n * top
+  int* active;    // slots with an expert
   void* out;
   hipStream_t stream;
 };

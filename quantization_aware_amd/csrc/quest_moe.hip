@@ -10,14 +10,17 @@
 //
 // With few tokens the chosen experts' weights are the work, and each is read once.
 // The grids count the most experts that can be chosen ("slots", min(experts, n top_k)),
-// since the choice is known on the device only; every workgroup finds its slot's
-// expert and that expert's tokens from the logits.  Kernels:
-//   gated    (some tiles of 16 columns of h, slot): the waves share k, sums meet in
-//            LDS; h goes to the workspace, a row for each token and expert rank;
+// since the choice is known on the device only.  Kernels:
+//   route    one workgroup: each token's experts and their weights; each slot's expert
+//            and its tokens;
+//   gated    (some tiles of 16 columns of h, slot): h goes to the workspace, a row for
+//            each token and rank of the expert among the token's;
 //   (h is quantised)
 //   down     (some tiles of 32 output columns, slot): the same of h's codes by down;
 //   combine  the top_k products of each token, weighted, in the order of their rank.
 // No atomics on results: the sums' order is fixed.  The workspace need not be set.
+// (With the choice found by every workgroup of gated and down instead of the first
+// kernel, their code is some 20 KB, and one token's gated kernel took 17.5 us.)
 #include <type_traits>
 
 #include "quest_device.h"
@@ -27,17 +30,18 @@
 namespace quest {
 namespace {
 
-constexpr int kMaxTokens = 64;   // one wave's lanes
-constexpr int kSets = 4;         // 64 experts each: 256 in all
+constexpr int kSets = kMoeMaxExperts / 64;  // of 64 experts
 constexpr int kWaves = 8;
 constexpr float kNone = -__builtin_inff();
 
-struct List {
-  int token[kMaxTokens];  // token | rank << 8 of the slot's expert, in the tokens' order
-  int rank_of[kMaxTokens];
-  uint32_t chosen[2 * kSets];  // a bit for each expert that some token takes
-  int count;
-};
+// A workgroup barrier that waits for this wave's LDS accesses only: loads of weights
+// stay in flight across it (a __syncthreads waits for them).
+__device__ __forceinline__ void lds_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // A token's logits as they lie in memory, expert 64 i + lane in raw[i] (past the last:
 // the last again).  Kept apart from their use, so that several tokens' loads overlap.
@@ -108,281 +112,285 @@ __device__ __forceinline__ int take_largest(float (&v)[kSets], int lane, float& 
   return e;
 }
 
-// How many experts come before e for a token, or -1 where e is none of its first top.
-__device__ __forceinline__ int rank_of(const float (&v)[kSets], int e, int top, int lane) {
-  float own = kNone;
-#pragma unroll
-  for (int i = 0; i < kSets; ++i)
-    if ((e >> 6) == i) own = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[i]), e & 63));
-  int before = 0;
-#pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    const int j = 64 * i + lane;
-    before += __builtin_popcountll(__builtin_amdgcn_ballot_w64(v[i] > own || (v[i] == own && j < e)));
-  }
-  return own != kNone && before < top ? before : -1;
-}
-
-// The slot's expert and its tokens, for a workgroup of kWaves waves; returns the
-// expert, or -1 for a slot without one.  Fewer slots than experts: slot s is the
-// s-th expert that any token takes; otherwise it is expert s.  A wave looks at up to
-// kEach tokens, whose logits it loads together.
-constexpr int kEach = kMaxTokens / kWaves;
-__device__ __forceinline__ int find_tokens(const MoeLaunch& a, int slot, List& list, int tid) {
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
-  const bool compact = a.slots < a.experts;
-  int e = slot;
-  float v[kEach][kSets];
-  {
-    uint32_t raw[kEach][kSets];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i * kWaves < a.n) fetch_logits(a, min(wave + i * kWaves, a.n - 1), lane, raw[i]);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i * kWaves < a.n) decode_logits(a, lane, raw[i], v[i]);
-  }
-  if (compact) {
-    if (tid < 2 * kSets) list.chosen[tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (wave + i * kWaves < a.n) {
-        float left[kSets];
-#pragma unroll
-        for (int j = 0; j < kSets; ++j) left[j] = v[i][j];
-        for (int r = 0; r < a.top; ++r) {
-          float value;
-          const int found = take_largest(left, lane, value);
-          if (found < 0) break;
-          if (lane == 0) atomicOr(&list.chosen[found >> 5], 1u << (found & 31));
-        }
-      }
-    __syncthreads();
-    int left = slot;
-    e = -1;
-#pragma unroll
-    for (int w = 0; w < 2 * kSets; ++w) {
-      uint32_t bits = __builtin_amdgcn_readfirstlane(list.chosen[w]);
-      const int here = __builtin_popcount(bits);
-      if (e < 0) {
-        if (left < here) {
-          for (; left > 0; --left) bits &= bits - 1;
-          e = 32 * w + __builtin_ctz(bits);
-        } else {
-          left -= here;
-        }
-      }
-    }
-    if (e < 0) return -1;
-  }
+constexpr int kRouteWaves = 16, kEach = kMoeMaxTokens / kRouteWaves;  // tokens a wave
+__global__ void __launch_bounds__(64 * kRouteWaves) quest_moe_route_kernel(const MoeLaunch a) {
+  __shared__ uint32_t takes[kMoeMaxExperts][2];  // a bit for each token that takes the expert
+  __shared__ uint8_t rank[kMoeMaxTokens][kMoeMaxExperts];
+  __shared__ int before[kSets + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
+  uint32_t raw[kEach][kSets];
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
-    if (wave + i * kWaves < a.n) {
-      const int r = rank_of(v[i], e, a.top, lane);
-      if (lane == 0) list.rank_of[wave + i * kWaves] = r;
-    }
+    if (i * kRouteWaves < a.n) fetch_logits(a, min(wave + i * kRouteWaves, a.n - 1), lane, raw[i]);
+  if (tid < 2 * kMoeMaxExperts) takes[tid >> 1][tid & 1] = 0;
   __syncthreads();
-  if (wave == 0) {
-    const int r = lane < a.n ? list.rank_of[lane] : -1;
-    const uint64_t takes = __builtin_amdgcn_ballot_w64(r >= 0);
-    if (r >= 0) list.token[__builtin_popcountll(takes & ((uint64_t(1) << lane) - 1))] = lane | r << 8;
-    if (lane == 0) list.count = __builtin_popcountll(takes);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int t = wave + i * kRouteWaves;
+    if (t >= a.n) break;
+    float v[kSets];
+    const bool nan = __builtin_amdgcn_ballot_w64(decode_logits(a, lane, raw[i], v)) != 0;
+    const float largest = wave_max(max_of(v));
+    // No product of a token with a NaN or +infinity is used: its output is NaN.
+    const bool undefined = nan || largest == __builtin_inff();
+    float all = 0.0f;
+    if (a.over_all)
+#pragma unroll
+      for (int j = 0; j < kSets; ++j) all += v[j] == kNone ? 0.0f : expf(v[j] - largest);
+    int found = 0;
+    float own = 0.0f;  // lane r: the exponential of the expert of rank r
+    for (; found < a.top && !undefined; ++found) {
+      float value;
+      const int e = take_largest(v, lane, value);
+      if (e < 0) break;
+      if (lane == 0) {
+        atomicOr(&takes[e][t >> 5], 1u << (t & 31));
+        rank[t][e] = static_cast<uint8_t>(found);
+      }
+      if (lane == found) own = expf(value - largest);
+    }
+    const float sum = group_sum(a.over_all ? all : own, 6);
+    if (lane < found) a.weight[t * a.top + lane] = own / sum;
+    if (lane == 0) a.found[t] = undefined ? -1 : found;
   }
   __syncthreads();
-  return e;
+  // Thread e < 256: expert e's slot is the number of chosen experts before it.
+  uint64_t mine = 0;
+  int below = 0;
+  if (tid < kMoeMaxExperts) {
+    mine = takes[tid][0] | static_cast<uint64_t>(takes[tid][1]) << 32;
+    const uint64_t used = __builtin_amdgcn_ballot_w64(mine != 0);
+    below = __builtin_popcountll(used & ((uint64_t(1) << lane) - 1));
+    if (lane == 0) before[wave] = __builtin_popcountll(used);
+  }
+  __syncthreads();
+  if (tid >= kMoeMaxExperts) return;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    if (i < wave) below += before[i];
+    total += before[i];
+  }
+  if (tid == 0) *a.active = total;
+  if (mine) {
+    MoeSlot& s = a.slot[below];
+    s.expert = tid;
+    s.count = __builtin_popcountll(mine);
+    for (int i = 0; mine; ++i, mine &= mine - 1) {
+      const int t = __builtin_ctzll(mine);
+      s.entry[i] = static_cast<uint16_t>(t | rank[t][tid] << 8);
+    }
+  }
 }
 
-__device__ __forceinline__ float activation(float g, int act) {
-  if (act == 0) return g / (1.0f + expf(-g));
+template <int kAct>
+__device__ __forceinline__ float activation(float g) {
+  if constexpr (kAct == 0) return g / (1.0f + expf(-g));
   return g * (0.5f * erfcf(g * -0.70710678f));
 }
 
 // Products of one slot's tokens by its expert's rows, T groups of 16 tokens at a time:
-// gated (h of 16 columns a tile, from gate and up) or down (32 columns a tile).  A
-// wave takes every 8th chunk of the contraction; its tokens' chunks, up to NC, stay in
-// its registers while the workgroup walks tiles tile0, tile0 + gridDim.x, ..., and
-// its loads of weights run kAhead chunks ahead, into the next tile.  NC = 0: any
-// length, the tokens' chunks read again for every tile.
-template <bool kPacked, int T, int NC, bool kGated>
-__global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const MoeLaunch a) {
-  constexpr int F = kFewFrags<kPacked>, kChunk = kFewChunk<kPacked>;
-  constexpr int kCols = kGated ? 16 : 32;
-  __shared__ List list;
-  __shared__ __attribute__((aligned(16))) uint32_t part[2][kWaves][2][T * 256];
+// gated (a tile is 16 columns of h: a strip of 16 rows of gate and one of up) or down
+// (32 columns: two strips).  KS waves share a tile, taking every KS-th chunk of the
+// contraction, and the workgroup's 8 / KS tiles at a time make one step of its walk.
+// The tokens' codes lie in LDS in the order of the fragments; where they do not fit
+// (`segment` chunks at a time), they are brought again for every step.  A wave's loads of
+// weights go straight to its registers and run kAhead chunks ahead, into its next tile:
+// with KS = 1 no wave waits for another.
+// kMode: kDown, or the gated product's activation.
+constexpr int kDown = -1;
+template <bool kPacked, int T, int KS, int kMode>
+__global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const MoeLaunch a, int segment) {
+  constexpr bool kGated = kMode != kDown;
+  constexpr int F = kFewFrags<kPacked>, kChunk = kFewChunk<kPacked>, kAhead = 4;
+  constexpr int kCols = kGated ? 16 : 32, kTiles = kWaves / KS;
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
+  __shared__ uint16_t entries[kMoeMaxTokens];
+  __shared__ __attribute__((aligned(16))) uint32_t part[KS > 1 ? kWaves : 1][2][KS > 1 ? T * 256 : 1];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
-  const int e = find_tokens(a, blockIdx.y, list, tid);
-  if (e < 0) return;
-  const int count = __builtin_amdgcn_readfirstlane(list.count);
+  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6, ks = wave % KS;
   const int len = kGated ? a.k : a.m, rows = kGated ? a.m : a.k;
   const int tiles = rows / kCols, chunks = (len + kChunk - 1) / kChunk;
+  const int segments = (chunks + segment - 1) / segment, pitch = segment * kChunk + 16;
   const int64_t row_bytes = kPacked ? len / 2 : len;
+  if (static_cast<int>(blockIdx.y) >= *a.active) return;
+  const MoeSlot& slot = a.slot[blockIdx.y];
+  const int e = slot.expert, count = slot.count;
+  if (tid < count) entries[tid] = slot.entry[tid];
   const int64_t first = (static_cast<int64_t>(e) * rows + (lane & 15)) * row_bytes;
   const uint8_t* const wide[2] = {(kGated ? a.gate : a.down) + first,
                                   kGated ? a.up + first : a.down + first + 16 * row_bytes};
   // Lanes of the last chunk's upper half may lie past the row: they read its first bytes
-  // (at_end) and count as zeros.
+  // and count as zeros.
   const bool short_end = kPacked && (len & 127) != 0 && (lane & 32);
-  const int at = 16 * g, at_end = short_end ? 0 : at;
-  int buf = 0;
+  const int mine = (chunks - ks + KS - 1) / KS;             // the wave's chunks ks, ks + KS, ...
+  const int steps = (mine + kAhead - 1) / kAhead * kAhead;  // in whole rounds of the ring
+  const int stride = gridDim.x * kTiles;
+  v4i w[kAhead][2];
+  auto load = [&](int tile, int i, v4i (&to)[2]) {
+    if (i < mine && tile < tiles) {
+      const int chunk = ks + i * KS;
+      const int64_t off = static_cast<int64_t>(tile) * kCols * row_bytes + chunk * 64 +
+                          (short_end && chunk == chunks - 1 ? 0 : 16 * g);
+      to[0] = load_v4i(wide[0] + off);
+      to[1] = load_v4i(wide[1] + off);
+    }
+  };
+  int tile = blockIdx.x * kTiles + wave / KS;
+  auto begin = [&]() {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(tile, i, w[i]);
+  };
+  begin();
+  lds_sync();
   for (int t0 = 0; t0 < count; t0 += 16 * T) {
-    const uint8_t* xp[T];
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      // (past the last token: the last again, whose sums are not used)
-      const int entry = list.token[min(t0 + 16 * t + (lane & 15), count - 1)];
-      xp[t] = kGated ? a.x + static_cast<int64_t>(entry & 255) * len
-                     : a.hc + (static_cast<int64_t>(entry & 255) * a.top + (entry >> 8)) * len;
-    }
-    constexpr int kRegs = NC ? NC : 1;
-    v4i fx[kRegs][T][F], token[T] = {};
-    if constexpr (NC > 0) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int chunk = c * kWaves + wave;
-        if (chunk < chunks) {
-          const bool off = short_end && chunk == chunks - 1;
-#pragma unroll
-          for (int t = 0; t < T; ++t) {
-            TokenBytes<kPacked> x;
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-              x.v[f] = load_v4i(xp[t] + chunk * kChunk + (off ? 0 : kChunk / 4 * g) + 16 * f);
-              if (off) x.v[f] = v4i{};
-            }
-            token_frags<kPacked>(x, fx[c][t]);
-          }
+    const int here = min(count - t0, 16 * T);
+    // Codes of chunks segment s on, 32 columns a thread at a time; columns past the row as zeros.
+    auto stage = [&](int s) {
+      const int blocks = min(segment, chunks - s * segment) * (kChunk / 32);
+      for (int j = tid; j < here * blocks; j += 64 * kWaves) {
+        const int i = j / blocks, c = (j - i * blocks) * 32, col = s * segment * kChunk + c;
+        const int entry = entries[t0 + i];
+        const uint8_t* x = kGated ? a.x + static_cast<int64_t>(entry & 255) * len
+                                  : a.hc + (static_cast<int64_t>(entry & 255) * a.top + (entry >> 8)) * len;
+        v4i v[2] = {};
+        if (col < len) v[0] = load_v4i(x + col), v[1] = load_v4i(x + col + 16);
+        if constexpr (kPacked) {
+          TokenBytes<true> b{{v[0], v[1]}};
+          token_frags<true>(b, v);
         }
-      }
-    }
-    constexpr int kAhead = NC == 0 ? 1 : NC < 4 ? NC : 4;
-    v4i w[kAhead][2];
-    auto load = [&](int tile, int c, v4i (&to)[2]) {
-      const int chunk = c * kWaves + wave;
-      if (chunk < chunks && tile < tiles) {
-        const int64_t off = static_cast<int64_t>(tile) * kCols * row_bytes + chunk * 64 +
-                            (chunk == chunks - 1 ? at_end : at);
-        to[0] = load_v4i(wide[0] + off);
-        to[1] = load_v4i(wide[1] + off);
+        v4i* to = reinterpret_cast<v4i*>(codes + i * pitch + c);
+        to[0] = v[0], to[1] = v[1];
       }
     };
-    if constexpr (NC > 0) {
+    if (t0 > 0) {
+      tile = blockIdx.x * kTiles + wave / KS;
+      begin();
+      lds_sync();  // the last group's codes have been read
+    }
+    stage(0);
+    lds_sync();
+    // (every wave makes the same steps: those without a tile only wait with the others)
+    for (int base = blockIdx.x * kTiles; base < tiles; base += stride, tile += stride) {
+      FewSums<kPacked, 2, T> s;
+      for (int seg = 0; seg < segments; ++seg) {
+        if (segments > 1 && (seg > 0 || base != static_cast<int>(blockIdx.x) * kTiles)) {
+          lds_sync();
+          stage(seg);
+          lds_sync();
+        }
+        const int last = seg + 1 < segments ? (seg + 1) * (segment / KS) : steps;
+        for (int i0 = seg * (segment / KS); i0 < last; i0 += kAhead) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) load(blockIdx.x, i, w[i]);
+          for (int r = 0; r < kAhead; ++r) {
+            const int i = i0 + r, chunk = ks + i * KS;
+            if (i < mine && tile < tiles) {
+              const bool off = short_end && chunk == chunks - 1;
+              v4i fw[2][F];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        if (c * kWaves + wave < chunks)
+              for (int p = 0; p < 2; ++p) wide_frags<kPacked>(off ? v4i{} : w[r][p], fw[p]);
+              const uint8_t* x = codes + (lane & 15) * pitch + (chunk - seg * segment) * kChunk + (kChunk / 4) * g;
+#pragma unroll
+              for (int f = 0; f < F; ++f) {
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                  const v4i fx = load_v4i(x + 16 * t * pitch + 16 * f);
+#pragma unroll
+                  for (int p = 0; p < 2; ++p) s.acc[p][t] = mfma_i8(fw[p][f], fx, s.acc[p][t]);
+                  s.token[t] = mfma_i8(ones_i8(), fx, s.token[t]);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) s.wide[p] = mfma_i8(fw[p][f], ones_i8(), s.wide[p]);
+              }
+            }
+            if (i + kAhead < steps)
+              load(tile, i + kAhead, w[r]);
+            else
+              load(tile + stride, i + kAhead - steps, w[r]);
+          }
+        }
+      }
+      // Four consecutive columns of a token: T_p of the strips to outputs.
+      auto finish = [&](int p, int i, int tile_, int c, v4u sum0, v4u sum1) {
+        const int entry = entries[t0 + i], row = (entry & 255) * a.top + (entry >> 8);
+        const int col = tile_ * kCols + 16 * p + c;
+        const int64_t ws = static_cast<int64_t>(e) * rows + col;
+        const uint32_t add = few_constant<kPacked>(len);
+        float y[4];
+        if constexpr (kGated) {
+          const float x_step = a.sx[entry & 255] * a.kx;
+          const float4 sg = *reinterpret_cast<const float4*>(a.sg + ws), su = *reinterpret_cast<const float4*>(a.su + ws);
+          const float fg[4] = {sg.x, sg.y, sg.z, sg.w}, fu[4] = {su.x, su.y, su.z, su.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float gv = (static_cast<float>(static_cast<int>(sum0[q] + add)) * 0.25f) * (x_step * (fg[q] * a.kw));
+            const float uv = (static_cast<float>(static_cast<int>(sum1[q] + add)) * 0.25f) * (x_step * (fu[q] * a.kw));
+            y[q] = activation<kMode>(gv) * uv;
+          }
+        } else {
+          const float x_step = a.hs[row] * a.kh;
+          const float4 sd = *reinterpret_cast<const float4*>(a.sd + ws);
+          const float fd[4] = {sd.x, sd.y, sd.z, sd.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            y[q] = (static_cast<float>(static_cast<int>(sum0[q] + add)) * 0.25f) * (x_step * (fd[q] * a.kw));
+        }
+        float* to = (kGated ? a.h : a.y) + static_cast<int64_t>(row) * rows + col;
+        *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+      };
+      if constexpr (KS == 1) {
+        if (tile < tiles)
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            const int i = 16 * t + (lane & 15);
+            if (i < here) {
+              finish(0, i, tile, 4 * g, s.total(0, t), s.total(1, t));
+              if (!kGated) finish(1, i, tile, 4 * g, s.total(1, t), v4u{});
+            }
+          }
+      } else {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int t = 0; t < T; ++t)
+            *reinterpret_cast<v4u*>(&part[wave][p][(16 * t + (lane & 15)) * 16 + 4 * g]) = s.total(p, t);
+        lds_sync();
+        // Quads of the step's outputs: tile, (down: strip,) token, 4 columns.
+        constexpr int kStrips = kGated ? 1 : 2;
+        for (int o = tid; o < kTiles * kStrips * T * 64; o += 64 * kWaves) {
+          const int q = o % (T * 64), p = kGated ? 0 : o / (T * 64) % 2, of = o / (T * 64 * kStrips);
+          const int i = q / 4;
+          if (i >= here || base + of >= tiles) continue;
+          v4u sum0 = {}, sum1 = {};
 #pragma unroll
-            for (int f = 0; f < F; ++f) token[t] = mfma_i8(ones_i8(), fx[c][t][f], token[t]);
-    }
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      FewSums<kPacked, 2, T> s;
-      if constexpr (NC > 0) {
-#pragma unroll
-        for (int t = 0; t < T; ++t) s.token[t] = token[t];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          constexpr int kMod = kAhead;
-          const int chunk = c * kWaves + wave;
-          if (chunk < chunks) {
-            v4i fw[2][F];
-            const bool off = short_end && chunk == chunks - 1;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) wide_frags<kPacked>(off ? v4i{} : w[c % kMod][p], fw[p]);
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-#pragma unroll
-                for (int t = 0; t < T; ++t) s.acc[p][t] = mfma_i8(fw[p][f], fx[c][t][f], s.acc[p][t]);
-                s.wide[p] = mfma_i8(fw[p][f], ones_i8(), s.wide[p]);
-              }
+          for (int j = 0; j < KS; ++j) {
+            sum0 += *reinterpret_cast<const v4u*>(&part[of * KS + j][p][4 * q]);
+            if (kGated) sum1 += *reinterpret_cast<const v4u*>(&part[of * KS + j][1][4 * q]);
           }
-          if (c + kAhead < NC)
-            load(tile, c + kAhead, w[c % kMod]);
-          else
-            load(tile + gridDim.x, c + kAhead - NC, w[c % kMod]);
+          finish(p, i, base + of, 4 * (q % 4), sum0, sum1);
         }
-      } else {
-        const int64_t off = static_cast<int64_t>(tile) * kCols * row_bytes;
-        const uint8_t* const wp[2] = {wide[0] + off, wide[1] + off};
-        few_run<kPacked, 2, T, 2>(s, wp, xp, wave, kWaves, chunks, len, lane);
+        lds_sync();
       }
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-          *reinterpret_cast<v4u*>(&part[buf][wave][p][(16 * t + (lane & 15)) * 16 + 4 * g]) = s.total(p, t);
-      __syncthreads();
-      // (the buffer is written again after the next tile's barrier, which follows these reads)
-      auto sum = [&](int p, int o) {
-        uint32_t v = few_constant<kPacked>(len);
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) v += part[buf][i][p][o];
-        return static_cast<float>(static_cast<int>(v)) * 0.25f;
-      };
-      for (int o = tid; o < (kGated ? 1 : 2) * T * 256; o += 64 * kWaves) {
-        const int p = kGated ? 0 : o / (T * 256), q = o % (T * 256);
-        const int i = t0 + q / 16, col = tile * kCols + 16 * p + q % 16;
-        if (i >= count) continue;
-        const int entry = list.token[i], row = (entry & 255) * a.top + (entry >> 8);
-        const int64_t ws = static_cast<int64_t>(e) * rows + col;
-        if constexpr (kGated) {
-          const float fx_ = a.sx[entry & 255] * a.kx;
-          const float gv = sum(0, q) * (fx_ * (a.sg[ws] * a.kw)), uv = sum(1, q) * (fx_ * (a.su[ws] * a.kw));
-          a.h[static_cast<int64_t>(row) * rows + col] = activation(gv, a.act) * uv;
-        } else {
-          a.y[static_cast<int64_t>(row) * rows + col] = sum(p, q) * ((a.hs[row] * a.kh) * (a.sd[ws] * a.kw));
-        }
-      }
-      buf ^= 1;
     }
   }
 }
 
 // Four columns a thread: the products of a token's experts, weighted, in the order of
-// their rank.  Every wave finds the token's weights itself.
+// their rank.
 template <typename Out>
 __global__ void __launch_bounds__(256) quest_moe_combine_kernel(const MoeLaunch a) {
-  __shared__ float weight[4][kMoeMaxTop];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x) >> 6;
-  const int t = blockIdx.y;
-  uint32_t raw[kSets];
-  float v[kSets];
-  fetch_logits(a, t, lane, raw);
-  const bool nan = __builtin_amdgcn_ballot_w64(decode_logits(a, lane, raw, v)) != 0;
-  const float largest = wave_max(max_of(v));
-  float sum = 0.0f;
-  if (a.over_all) {
-#pragma unroll
-    for (int i = 0; i < kSets; ++i) sum += v[i] == kNone ? 0.0f : expf(v[i] - largest);
-    sum = group_sum(sum, 6);
-  }
-  int found = 0;
-  for (; found < a.top; ++found) {
-    float value;
-    if (take_largest(v, lane, value) < 0) break;
-    const float p = expf(value - largest);
-    if (!a.over_all) sum += p;
-    if (lane == 0) weight[wave][found] = p;
-  }
-  const float inv = 1.0f / sum;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (c >= a.k) return;
+  const int found = a.found[t];
   float y[4] = {};
   const float* part = a.y + static_cast<int64_t>(t) * a.top * a.k + c;
   for (int r = 0; r < found; ++r) {
-    const float p = weight[wave][r] * inv;
+    const float p = a.weight[t * a.top + r];
     const float4 w = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(r) * a.k);
     y[0] = fmaf(p, w.x, y[0]), y[1] = fmaf(p, w.y, y[1]), y[2] = fmaf(p, w.z, y[2]), y[3] = fmaf(p, w.w, y[3]);
   }
-  if (nan) y[0] = y[1] = y[2] = y[3] = __builtin_nanf("");
+  if (found < 0) y[0] = y[1] = y[2] = y[3] = __builtin_nanf("");
   Out* out = static_cast<Out*>(a.out) + static_cast<int64_t>(t) * a.k + c;
   if constexpr (sizeof(Out) == 2)
     *reinterpret_cast<u32x2*>(out) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
@@ -390,42 +398,54 @@ __global__ void __launch_bounds__(256) quest_moe_combine_kernel(const MoeLaunch 
     *reinterpret_cast<float4*>(out) = make_float4(y[0], y[1], y[2], y[3]);
 }
 
-template <bool kPacked, int T, int NC, bool kGated>
-hipError_t launch_product(const MoeLaunch& a) {
-  const int tiles = kGated ? a.m / 16 : a.k / 32;
-  // Workgroups walk tiles so that finding the tokens is paid once for several, down to
-  // about four workgroups a compute unit.
-  const int64_t total = static_cast<int64_t>(tiles) * a.slots;
-  const int walk = static_cast<int>((total + 1023) / 1024);
-  hipLaunchKernelGGL((quest_moe_product_kernel<kPacked, T, NC, kGated>), dim3((tiles + walk - 1) / walk, a.slots),
-                     dim3(64 * kWaves), 0, a.stream, a);
+template <bool kPacked, int T, int KS, int kMode>
+hipError_t launch_product(const MoeLaunch& a, int tiles, int chunks) {
+  constexpr int kChunk = kFewChunk<kPacked>, kTiles = kWaves / KS;
+  // All chunks at a time if they fit in LDS, else whole rounds of every wave's ring of loads.
+  constexpr int kLds = 159 * 1024 - (KS > 1 ? kWaves * 2 * T * 1024 : 0);  // of 160 KB, beside the sums
+  constexpr int kFit = (kLds / (16 * T) - 16) / kChunk, kRound = 4 * KS, kMost = kFit / kRound * kRound;
+  static_assert(kMost >= kRound, "a segment holds a round");
+  int segment = chunks;
+  if (chunks > kFit) {
+    const int parts = (chunks + kMost - 1) / kMost;
+    segment = ((chunks + parts - 1) / parts + kRound - 1) / kRound * kRound;
+  }
+  const size_t lds = static_cast<size_t>(16 * T) * (segment * kChunk + 16);
+  // Workgroups walk tiles, so that finding and bringing the tokens is paid once for
+  // several, down to about three workgroups a compute unit.
+  const int each = (tiles + kTiles - 1) / kTiles;
+  const int walk = static_cast<int>((static_cast<int64_t>(each) * a.slots + 767) / 768);
+  hipLaunchKernelGGL((quest_moe_product_kernel<kPacked, T, KS, kMode>), dim3((each + walk - 1) / walk, a.slots),
+                     dim3(64 * kWaves), lds, a.stream, a, segment);
   return hipGetLastError();
 }
 
-template <bool kPacked, bool kGated>
+template <bool kPacked, int kMode>
 hipError_t launch_products(const MoeLaunch& a) {
+  constexpr bool kGated = kMode != kDown;
   // Two groups of 16 tokens at once where an expert has more than 10 on average.
   const bool two = static_cast<int64_t>(a.n) * a.top > 10 * static_cast<int64_t>(a.experts);
+  const int tiles = kGated ? a.m / 16 : a.k / 32;
   const int chunks = ((kGated ? a.k : a.m) + kFewChunk<kPacked> - 1) / kFewChunk<kPacked>;
-  const int each = (chunks + kWaves - 1) / kWaves;
-  auto run = [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    if constexpr (!kPacked || NC < 8)  // (two groups' codes of 8192 columns do not fit the registers)
-      if (two) return launch_product<kPacked, 2, NC, kGated>(a);
-    return launch_product<kPacked, 1, NC, kGated>(a);
+  auto run = [&](auto ks) {
+    constexpr int KS = decltype(ks)::value;
+    return two ? launch_product<kPacked, 2, KS < 8 ? KS : 4, kMode>(a, tiles, chunks)
+               : launch_product<kPacked, 1, KS, kMode>(a, tiles, chunks);
   };
-  if (each <= 2) return run(std::integral_constant<int, 2>{});
-  if (each <= 4) return run(std::integral_constant<int, 4>{});
-  if (each <= 8) return run(std::integral_constant<int, 8>{});
-  if constexpr (!kPacked)
-    if (each <= 16) return run(std::integral_constant<int, 16>{});
-  if constexpr (kGated) return launch_product<kPacked, 1, 0, true>(a);
-  return hipErrorInvalidValue;  // (down's length is at most kMoeMaxWidth)
+  // As few waves a tile as keep some 16 waves a compute unit busy.
+  const int64_t waves = static_cast<int64_t>(tiles) * a.slots;
+  if (waves >= 4096 || chunks < 2) return run(std::integral_constant<int, 1>{});
+  if (waves >= 2048 || chunks < 4) return run(std::integral_constant<int, 2>{});
+  if (waves >= 1024 || chunks < 8) return run(std::integral_constant<int, 4>{});
+  return run(std::integral_constant<int, 8>{});
 }
 
 template <bool kPacked>
 hipError_t launch(const MoeLaunch& a, bool out_bf16) {
-  hipError_t err = launch_products<kPacked, true>(a);
+  hipLaunchKernelGGL(quest_moe_route_kernel, dim3(1), dim3(64 * kRouteWaves), 0, a.stream, a);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  err = a.act == 0 ? launch_products<kPacked, 0>(a) : launch_products<kPacked, 1>(a);
   if (err != hipSuccess) return err;
   FwdLaunch q;
   q.rows = static_cast<int64_t>(a.n) * a.top;
@@ -440,7 +460,7 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
   q.stream = a.stream;
   err = launch_fwd_i8(a.h, 0, a.log_block, a.h_bits, q);
   if (err != hipSuccess) return err;
-  err = launch_products<kPacked, false>(a);
+  err = launch_products<kPacked, kDown>(a);
   if (err != hipSuccess) return err;
   const dim3 grid((a.k + 1023) / 1024, a.n);
   if (out_bf16)
