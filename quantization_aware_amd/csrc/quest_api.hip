@@ -530,7 +530,7 @@ quest_status quest_gemm_i8(const int8_t* a, const float* a_scale, int64_t m, int
   g.sb = b_scale;
   g.n = static_cast<int>(n);
   g.k = static_cast<int>(k);
-  g.ka = step_factor(a_bits);
+  g.ka = 0.25f * step_factor(a_bits);
   g.kb = step_factor(b_bits);
   g.out = out;
   g.stream = static_cast<hipStream_t>(stream);

@@ -116,49 +116,30 @@ __device__ __forceinline__ uint32_t few_constant(int k) {
   return static_cast<uint32_t>(kPacked ? -15 * k : k);
 }
 
-// Adds chunks first, first + stride, ... of `chunks` to the sums: wide rows at wp[p]
-// and tokens at xp[t] (the lane's rows, their chunk 0), kAhead chunks' loads in
-// flight.  In the last chunk of 128 the upper half may lie past k (a multiple of 64):
-// those lanes (64 (l / 32) of it) read the chunk's first bytes and count as zeros.
-template <bool kPacked, int P, int T, int kAhead>
-__device__ __forceinline__ void few_run(FewSums<kPacked, P, T>& s, const uint8_t* const (&wp)[P],
-                                        const uint8_t* const (&xp)[T], int first, int stride, int chunks, int k,
-                                        int lane) {
-  constexpr int kW = 64;  // bytes of a wide row's chunk
-  constexpr int kX = kFewChunk<kPacked>;
-  const int g = lane >> 4;
-  auto live = [&](int c) { return !kPacked || c * 128 + 32 * g < k; };
-  auto load = [&](int c, v4i (&w)[P], TokenBytes<kPacked> (&x)[T]) {
-    const int64_t at = static_cast<int64_t>(c);
-    const int gl = live(c) ? g : 0;
-#pragma unroll
-    for (int p = 0; p < P; ++p) w[p] = load_v4i(wp[p] + at * kW + 16 * gl);
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int f = 0; f < kFewFrags<kPacked>; ++f)
-        x[t].v[f] = load_v4i(xp[t] + at * kX + (kX / 4) * gl + 16 * f);
+// Adds chunks first, first + stride, ... of `chunks` of signed byte codes to the sums:
+// the lane's wide row at w, its token at x; four chunks' loads in flight.
+__device__ __forceinline__ void few_run(FewSums<false, 1, 1>& s, const uint8_t* w, const uint8_t* x, int first,
+                                        int stride, int chunks, int lane) {
+  constexpr int kAhead = 4;
+  w += 16 * (lane >> 4);
+  x += 16 * (lane >> 4);
+  v4i fw[kAhead][1];
+  TokenBytes<false> fx[kAhead][1];
+  auto load = [&](int c, int i) {
+    if (c >= chunks) return;
+    fw[i][0] = load_v4i(w + static_cast<int64_t>(c) * 64);
+    fx[i][0].v[0] = load_v4i(x + static_cast<int64_t>(c) * 64);
   };
-  v4i w[kAhead][P];
-  TokenBytes<kPacked> x[kAhead][T];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (first + i * stride < chunks) load(first + i * stride, w[i], x[i]);
+  for (int i = 0; i < kAhead; ++i) load(first + i * stride, i);
   for (int c = first; c < chunks; c += kAhead * stride) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int ci = c + i * stride;
       if (ci < chunks) {
-        v4i cw[P];
-        TokenBytes<kPacked> cx[T];
-        const bool on = live(ci);
-#pragma unroll
-        for (int p = 0; p < P; ++p) cw[p] = on ? w[i][p] : v4i{};
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-          for (int f = 0; f < kFewFrags<kPacked>; ++f) cx[t].v[f] = on ? x[i][t].v[f] : v4i{};
-        if (ci + kAhead * stride < chunks) load(ci + kAhead * stride, w[i], x[i]);
+        const v4i cw[1] = {fw[i][0]};
+        const TokenBytes<false> cx[1] = {fx[i][0]};
+        load(ci + kAhead * stride, i);
         s.add(cw, cx);
       }
     }

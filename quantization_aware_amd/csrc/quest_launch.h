@@ -225,8 +225,8 @@ struct GemmI8Launch {
   const float* sb;
   int n;
   int k;     // a multiple of 64, up to 32768
-  float ka;  // 2 / (L_a - 1)
-  float kb;
+  float ka;  // a quarter of 2 / (L_a - 1): the sums are of odd numbers
+  float kb;  // 2 / (L_b - 1)
   void* out;
   hipStream_t stream;
 };
