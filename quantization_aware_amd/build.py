@@ -33,6 +33,7 @@ SOURCES = [
     "quest_i8.hip",
     "quest_gemm_i8.hip",
     "quest_moe.hip",
+    "quest_moe_few.hip",
 ]
 # Sources built without the VGPR-only MFMA form, leaving the placement of the
 # matrix-core accumulators to the register allocator (the product kernels, whose

@@ -28,6 +28,18 @@ constexpr int kFewChunk = kPacked ? 128 : 64;
 template <bool kPacked>
 constexpr int kFewFrags = kPacked ? 2 : 1;
 
+// 16 bytes at `off` of a window of memory: zeros past its end, kNoBytes always so.  With
+// a branch around a load the compiler no longer knows how many are on their way, and
+// waits for all of them before it uses one.
+constexpr int kNoBytes = 0x7FFFFFF0;
+typedef __amdgpu_buffer_rsrc_t few_rsrc;
+__device__ __forceinline__ few_rsrc few_window(const uint8_t* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), static_cast<short>(0), bytes, 0x00020000);
+}
+__device__ __forceinline__ v4i load_window(few_rsrc r, int off) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 __device__ __forceinline__ v4i load_v4i(const uint8_t* p) { return *reinterpret_cast<const v4i*>(p); }
 
 // A lane's 16 bytes of a wide row's chunk as fragments.
@@ -116,34 +128,30 @@ __device__ __forceinline__ uint32_t few_constant(int k) {
   return static_cast<uint32_t>(kPacked ? -15 * k : k);
 }
 
-// Adds chunks first, first + stride, ... of `chunks` of signed byte codes to the sums:
-// the lane's wide row at w, its token at x; four chunks' loads in flight.
-__device__ __forceinline__ void few_run(FewSums<false, 1, 1>& s, const uint8_t* w, const uint8_t* x, int first,
-                                        int stride, int chunks, int lane) {
-  constexpr int kAhead = 4;
-  w += 16 * (lane >> 4);
-  x += 16 * (lane >> 4);
-  v4i fw[kAhead][1];
-  TokenBytes<false> fx[kAhead][1];
-  auto load = [&](int c, int i) {
-    if (c >= chunks) return;
-    fw[i][0] = load_v4i(w + static_cast<int64_t>(c) * 64);
-    fx[i][0].v[0] = load_v4i(x + static_cast<int64_t>(c) * 64);
-  };
+// A wave's walk over chunks first, first + stride, ... of `chunks`, kAhead of them on
+// their way: begin() issues the first loads; run() uses each chunk and issues the load
+// kAhead further on.  load(c, i) brings chunk c to place i (zeros for those behind the
+// last), use(c, i) takes it from there.
+template <int kAhead>
+struct FewRing {
+  int first, stride, chunks;
+
+  template <typename Load>
+  __device__ __forceinline__ void begin(Load load) const {
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(first + i * stride, i);
-  for (int c = first; c < chunks; c += kAhead * stride) {
+    for (int i = 0; i < kAhead; ++i) load(first + i * stride, i);
+  }
+  template <typename Load, typename Use>
+  __device__ __forceinline__ void run(Load load, Use use) const {
+    for (int c = first; c < chunks; c += kAhead * stride) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int ci = c + i * stride;
-      if (ci < chunks) {
-        const v4i cw[1] = {fw[i][0]};
-        const TokenBytes<false> cx[1] = {fx[i][0]};
+      for (int i = 0; i < kAhead; ++i) {
+        const int ci = c + i * stride;
+        if (ci < chunks) use(ci, i);
         load(ci + kAhead * stride, i);
-        s.add(cw, cx);
       }
     }
   }
-}
+};
 
 }  // namespace quest

@@ -351,11 +351,22 @@ __global__ void __launch_bounds__(512) quest_gemm_i8_few_kernel(const GemmI8Laun
   const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
   const int tokens = kSwap ? g.n : g.m, rows = kSwap ? g.m : g.n, k = g.k;
   const int row0 = blockIdx.x * 16;
-  // (past the last row: the last again, whose sums are not used)
-  const uint8_t* const wp = (kSwap ? g.a : g.b) + static_cast<int64_t>(min(row0 + (lane & 15), rows - 1)) * k;
-  const uint8_t* const xp = (kSwap ? g.b : g.a) + static_cast<int64_t>(min(lane & 15, tokens - 1)) * k;
+  // (rows past the last read as zeros)
+  const few_rsrc rw = few_window((kSwap ? g.a : g.b) + static_cast<int64_t>(row0) * k, min(rows - row0, 16) * k);
+  const few_rsrc rx = few_window(kSwap ? g.b : g.a, tokens * k);
+  const int at = (lane & 15) * k + 16 * (lane >> 4);
+  constexpr int kAhead = 4;
+  const FewRing<kAhead> ring{wave, kWaves, k / 64};
+  v4i fw[kAhead][1];
+  TokenBytes<false> fx[kAhead][1];
+  auto load = [&](int c, int i) {
+    const int off = c < ring.chunks ? at + c * 64 : kNoBytes;
+    fw[i][0] = load_window(rw, off);
+    fx[i][0].v[0] = load_window(rx, off);
+  };
   FewSums<false, 1, 1> s;
-  few_run(s, wp, xp, wave, kWaves, k / 64, lane);
+  ring.begin(load);
+  ring.run(load, [&](int, int i) { s.add(fw[i], fx[i]); });
   *reinterpret_cast<v4u*>(&part[wave][(lane & 15) * 16 + 4 * (lane >> 4)]) = s.total(0, 0);
   __syncthreads();
   const int token = tid / 16, row = row0 + tid % 16;

@@ -9,23 +9,12 @@
 // (and the one of y / Delta) move an entry across a level's edge; adding 2^(b-1)
 // first, as packed codes are made, rounds y / Delta to 2^-17 at b = 8 and moves
 // eight times as many.
-#include "quest_kernels.h"
+#include "quest_i8.h"
 
 namespace quest {
 namespace {
 
 extern __shared__ u32x4 i8_lds[];
-
-// Four values (in steps of Delta) to four signed bytes.
-__device__ __forceinline__ uint32_t codes4(const float* v, float kk, float half) {
-  int c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = static_cast<int>(__builtin_amdgcn_fmed3f(__builtin_floorf(v[j] * kk), -half, half - 1.0f));
-  const uint32_t lo = __builtin_amdgcn_perm(static_cast<uint32_t>(c[1]), static_cast<uint32_t>(c[0]), 0x0C0C0400u);
-  const uint32_t hi = __builtin_amdgcn_perm(static_cast<uint32_t>(c[3]), static_cast<uint32_t>(c[2]), 0x04000C0Cu);
-  return lo | hi;
-}
 
 // A workgroup holds rows_per_wg whole rows, a lane a run of 32 entries, as in
 // quest_fwd_rows_kernel; rows within a wave need no LDS for their sums.
@@ -117,15 +106,7 @@ __global__ void __launch_bounds__(256)
 template <typename In, int LOGN>
 hipError_t launch_fwd(const In* x, int bits, const FwdLaunch& a) {
   const int runs = static_cast<int>(a.cols / RUN);
-  const double n = double(1 << LOGN), levels = double(1 << bits);
-  FwdConsts k;  // as the packed forward's, with the number of levels at run time
-  k.alpha = static_cast<float>(a.alpha);
-  k.kk = static_cast<float>((levels - 1.0) / (2.0 * a.alpha * std::sqrt(n)));
-  k.thr = static_cast<float>(a.alpha * (1.0 + a.trust / (levels - 1.0)) * std::sqrt(n));
-  k.inv_cols = static_cast<float>(1.0 / double(a.cols));
-  k.chunks = 0;
-  int group = runs & -runs;
-  if (group > 64) group = 64;
+  const FwdConsts k = i8_consts(a.cols, LOGN, bits, a.alpha, a.trust);
   // Whole rows: the fewest that fill whole waves, and then up to 256 lanes.
   int rows_per_wg = 64 / gcd_int(runs, 64);
   if (rows_per_wg * runs > 1024) rows_per_wg = 1024 / runs;
@@ -135,7 +116,7 @@ hipError_t launch_fwd(const In* x, int bits, const FwdLaunch& a) {
   const int64_t grid = (a.rows + rows_per_wg - 1) / rows_per_wg;
   const size_t lds = static_cast<size_t>(threads) * (sizeof(In) * 32) + static_cast<size_t>(threads) * 4;
   hipLaunchKernelGGL((quest_fwd_i8_kernel<In, LOGN>), dim3(static_cast<uint32_t>(grid)), dim3(threads), lds, a.stream,
-                     x, a.rows, runs, rows_per_wg, log2_exact(group), k, static_cast<float>(1 << (bits - 1)), a.codes, a.scale,
+                     x, a.rows, runs, rows_per_wg, i8_log_group(runs), k, static_cast<float>(1 << (bits - 1)), a.codes, a.scale,
                      reinterpret_cast<uint32_t*>(a.mask));
   return hipGetLastError();
 }

@@ -11,184 +11,122 @@
 // With few tokens the chosen experts' weights are the work, and each is read once.
 // The grids count the most experts that can be chosen ("slots", min(experts, n top_k)),
 // since the choice is known on the device only.  Kernels:
-//   route    one workgroup: each token's experts and their weights; each slot's expert
-//            and its tokens;
-//   gated    (some tiles of 16 columns of h, slot): h goes to the workspace, a row for
-//            each token and rank of the expert among the token's;
+//   route    a wave for each token: its experts and their weights (all in one workgroup
+//            took 12 us for 64 tokens of top 8 of 128 instead of 4.8);
+//   gated    (some tiles of 16 columns of h, slot): first which expert the slot's is and
+//            which tokens take it; h goes to the workspace, a row for each token and rank
+//            of the expert among the token's;
 //   (h is quantised)
 //   down     (some tiles of 32 output columns, slot): the same of h's codes by down;
 //   combine  the top_k products of each token, weighted, in the order of their rank.
 // No atomics on results: the sums' order is fixed.  The workspace need not be set.
-// (With the choice found by every workgroup of gated and down instead of the first
-// kernel, their code is some 20 KB, and one token's gated kernel took 17.5 us.)
+//
+// What bounds it is reading the weights: 64 tokens of top 8 of 128 experts of 2048 x 768 at
+// 4 bits, 302 MB, take 42.8 us in gated and 24.6 in down, 4.7 and 4.1 TB/s (a copy of 2 GiB
+// reaches 4.84); of 8 experts of 2048 x 5632 at 8 bits, 277 MB, 48.0 and 25.4 (3.85 and
+// 3.6).  That needs every load issued without a branch around it: with one, each wait was
+// for all loads on their way, 50 and 26 us, 54 and 28.5.  The other three kernels are some
+// 5 us each.
 #include <type_traits>
 
-#include "quest_device.h"
 #include "quest_few.h"
 #include "quest_launch.h"
+#include "quest_moe.h"
 
 namespace quest {
 namespace {
 
-constexpr int kSets = kMoeMaxExperts / 64;  // of 64 experts
-constexpr int kWaves = 8;
-constexpr float kNone = -__builtin_inff();
+constexpr int kWaves = 8, kAhead = 4;  // chunks of weights on their way
 
-// A workgroup barrier that waits for this wave's LDS accesses only: loads of weights
-// stay in flight across it (a __syncthreads waits for them).
-__device__ __forceinline__ void lds_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+// A wave a token.  The choice goes where the kernel after the next puts products: the
+// expert of each rank, -1 for none.
+template <int S>
+__global__ void __launch_bounds__(64) quest_moe_route_kernel(const MoeLaunch a) {
+  const int t = blockIdx.x, lane = threadIdx.x;
+  uint32_t raw[S];
+  fetch_logits(a, t, lane, raw);
+  const Choice c = choose(a, lane, raw, a.top, true);
+  if (lane < a.top) reinterpret_cast<int16_t*>(a.y)[t * a.top + lane] = lane < c.found ? c.expert : -1;
+  if (lane < c.found) a.weight[t * a.top + lane] = c.weight;
+  if (lane == 0) a.found[t] = c.found;
 }
 
-// A token's logits as they lie in memory, expert 64 i + lane in raw[i] (past the last:
-// the last again).  Kept apart from their use, so that several tokens' loads overlap.
-__device__ __forceinline__ void fetch_logits(const MoeLaunch& a, int t, int lane, uint32_t (&raw)[kSets]) {
-  const int64_t row = static_cast<int64_t>(t) * a.experts;
+// Slot s of the chosen experts, in order of their index.  find() gives its expert, or -1
+// if there are fewer; collect() its tokens in order (token | rank << 8) and their count.
+// Every thread of the workgroup calls both.
+struct SlotSearch {
+  static constexpr int kThreads = 64 * kWaves, kEach = kMoeMaxTokens * kMoeMaxTop / kThreads;
+  struct Shared {
+    uint32_t used[kMoeMaxExperts / 32];  // a bit an expert
+    int expert;
+    int hits[kEach * kWaves];
+  };
+  const MoeLaunch& a;
+  Shared& sh;
+  int16_t mine[kEach];
+
+  __device__ __forceinline__ int find(int s) {
+    const int tid = threadIdx.x;
+    const int16_t* const choice = reinterpret_cast<const int16_t*>(a.y);
 #pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    raw[i] = 0;
-    if (64 * i < a.experts) {
-      const int64_t at = row + min(64 * i + lane, a.experts - 1);
-      if (a.logits_bf16)
-        raw[i] = static_cast<const uint16_t*>(a.logits)[at];
-      else
-        raw[i] = static_cast<const uint32_t*>(a.logits)[at];
+    for (int j = 0; j < kEach; ++j) {
+      const int p = tid + j * kThreads;
+      mine[j] = p < a.n * a.top ? choice[p] : -1;
     }
+    if (tid < kMoeMaxExperts / 32) sh.used[tid] = 0;
+    if (tid == 0) sh.expert = -1;
+    lds_sync();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (mine[j] >= 0) atomicOr(&sh.used[mine[j] >> 5], 1u << (mine[j] & 31));
+    lds_sync();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
+      const int in_w = __builtin_popcount(sh.used[w]);
+      if (w < tid >> 5) before += in_w;
+      total += in_w;
+    }
+    if (blockIdx.x == 0 && s == 0 && tid == 0) *a.active = total;
+    if (s >= total) return -1;
+    if (tid < kMoeMaxExperts) {
+      const uint32_t word = sh.used[tid >> 5];
+      before += __builtin_popcount(word & ((1u << (tid & 31)) - 1));
+      if ((word >> (tid & 31) & 1) && before == s) sh.expert = tid;
+    }
+    lds_sync();
+    return __builtin_amdgcn_readfirstlane(sh.expert);
   }
-}
 
-// Their values: -inf past the last expert, and for NaN (which no comparison finds; the
-// combining kernel gives NaN for such a token).  Returns whether the lane saw a NaN.
-__device__ __forceinline__ bool decode_logits(const MoeLaunch& a, int lane, const uint32_t (&raw)[kSets],
-                                              float (&v)[kSets]) {
-  const int shift = a.logits_bf16 ? 16 : 0;
-  bool nan = false;
+  __device__ __forceinline__ int collect(int e, uint16_t* entries) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint64_t at[kEach];
 #pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    const float f = __uint_as_float(raw[i] << shift);
-    nan |= f != f;
-    v[i] = 64 * i + lane < a.experts && f == f ? f : kNone;
-  }
-  return nan;
-}
-
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float x) {
-  return fmaxf(x, dpp_read<CTRL>(x));
-}
-
-// The largest of all lanes' (no NaN among them), the same in every lane.
-__device__ __forceinline__ float wave_max(float x) {
-  x = dpp_max<0xB1>(x);
-  x = dpp_max<0x4E>(x);
-  x = dpp_max<0x141>(x);
-  x = dpp_max<0x140>(x);  // every lane of a row of 16 has the row's
-  float r[4];
+    for (int j = 0; j < kEach; ++j) {
+      at[j] = __builtin_amdgcn_ballot_w64(mine[j] == e);
+      if (lane == 0) sh.hits[j * kWaves + wave] = __builtin_popcountll(at[j]);
+    }
+    lds_sync();
+    int count = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 16 * i));
-  return fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
-}
-
-__device__ __forceinline__ float max_of(const float (&v)[kSets]) {
-  return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-}
-
-// Takes the largest logit (of equal ones the lowest index) out of v: its expert, or -1.
-__device__ __forceinline__ int take_largest(float (&v)[kSets], int lane, float& value) {
-  value = wave_max(max_of(v));
-  if (value == kNone) return -1;
-  int e = -1;
+    for (int j = 0; j < kEach; ++j) {
+      if (j * kThreads >= a.n * a.top) break;
+      int before = count + __builtin_popcountll(at[j] & ((uint64_t(1) << lane) - 1));
 #pragma unroll
-  for (int i = kSets - 1; i >= 0; --i) {
-    const uint64_t at = __builtin_amdgcn_ballot_w64(v[i] == value);
-    if (at) e = 64 * i + __builtin_ctzll(at);
-  }
-#pragma unroll
-  for (int i = 0; i < kSets; ++i)
-    if (64 * i + lane == e) v[i] = kNone;
-  return e;
-}
-
-constexpr int kRouteWaves = 16, kEach = kMoeMaxTokens / kRouteWaves;  // tokens a wave
-__global__ void __launch_bounds__(64 * kRouteWaves) quest_moe_route_kernel(const MoeLaunch a) {
-  __shared__ uint32_t takes[kMoeMaxExperts][2];  // a bit for each token that takes the expert
-  __shared__ uint8_t rank[kMoeMaxTokens][kMoeMaxExperts];
-  __shared__ int before[kSets + 1];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid) >> 6;
-  uint32_t raw[kEach][kSets];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (i * kRouteWaves < a.n) fetch_logits(a, min(wave + i * kRouteWaves, a.n - 1), lane, raw[i]);
-  if (tid < 2 * kMoeMaxExperts) takes[tid >> 1][tid & 1] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int t = wave + i * kRouteWaves;
-    if (t >= a.n) break;
-    float v[kSets];
-    const bool nan = __builtin_amdgcn_ballot_w64(decode_logits(a, lane, raw[i], v)) != 0;
-    const float largest = wave_max(max_of(v));
-    // No product of a token with a NaN or +infinity is used: its output is NaN.
-    const bool undefined = nan || largest == __builtin_inff();
-    float all = 0.0f;
-    if (a.over_all)
-#pragma unroll
-      for (int j = 0; j < kSets; ++j) all += v[j] == kNone ? 0.0f : expf(v[j] - largest);
-    int found = 0;
-    float own = 0.0f;  // lane r: the exponential of the expert of rank r
-    for (; found < a.top && !undefined; ++found) {
-      float value;
-      const int e = take_largest(v, lane, value);
-      if (e < 0) break;
-      if (lane == 0) {
-        atomicOr(&takes[e][t >> 5], 1u << (t & 31));
-        rank[t][e] = static_cast<uint8_t>(found);
+      for (int w = 0; w < kWaves; ++w) {
+        const int h = sh.hits[j * kWaves + w];
+        if (w < wave) before += h;
+        count += h;
       }
-      if (lane == found) own = expf(value - largest);
+      if (mine[j] == e) {
+        const int p = tid + j * kThreads, t = p / a.top;
+        entries[before] = static_cast<uint16_t>(t | (p - t * a.top) << 8);
+      }
     }
-    const float sum = group_sum(a.over_all ? all : own, 6);
-    if (lane < found) a.weight[t * a.top + lane] = own / sum;
-    if (lane == 0) a.found[t] = undefined ? -1 : found;
+    lds_sync();
+    return count;
   }
-  __syncthreads();
-  // Thread e < 256: expert e's slot is the number of chosen experts before it.
-  uint64_t mine = 0;
-  int below = 0;
-  if (tid < kMoeMaxExperts) {
-    mine = takes[tid][0] | static_cast<uint64_t>(takes[tid][1]) << 32;
-    const uint64_t used = __builtin_amdgcn_ballot_w64(mine != 0);
-    below = __builtin_popcountll(used & ((uint64_t(1) << lane) - 1));
-    if (lane == 0) before[wave] = __builtin_popcountll(used);
-  }
-  __syncthreads();
-  if (tid >= kMoeMaxExperts) return;
-  int total = 0;
-#pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    if (i < wave) below += before[i];
-    total += before[i];
-  }
-  if (tid == 0) *a.active = total;
-  if (mine) {
-    MoeSlot& s = a.slot[below];
-    s.expert = tid;
-    s.count = __builtin_popcountll(mine);
-    for (int i = 0; mine; ++i, mine &= mine - 1) {
-      const int t = __builtin_ctzll(mine);
-      s.entry[i] = static_cast<uint16_t>(t | rank[t][tid] << 8);
-    }
-  }
-}
-
-template <int kAct>
-__device__ __forceinline__ float activation(float g) {
-  if constexpr (kAct == 0) return g / (1.0f + expf(-g));
-  return g * (0.5f * erfcf(g * -0.70710678f));
-}
+};
 
 // Products of one slot's tokens by its expert's rows, T groups of 16 tokens at a time:
 // gated (a tile is 16 columns of h: a strip of 16 rows of gate and one of up) or down
@@ -203,7 +141,7 @@ constexpr int kDown = -1;
 template <bool kPacked, int T, int KS, int kMode>
 __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const MoeLaunch a, int segment) {
   constexpr bool kGated = kMode != kDown;
-  constexpr int F = kFewFrags<kPacked>, kChunk = kFewChunk<kPacked>, kAhead = 4;
+  constexpr int F = kFewFrags<kPacked>, kChunk = kFewChunk<kPacked>;
   constexpr int kCols = kGated ? 16 : 32, kTiles = kWaves / KS;
   extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
   __shared__ uint16_t entries[kMoeMaxTokens];
@@ -213,29 +151,35 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
   const int len = kGated ? a.k : a.m, rows = kGated ? a.m : a.k;
   const int tiles = rows / kCols, chunks = (len + kChunk - 1) / kChunk;
   const int segments = (chunks + segment - 1) / segment, pitch = segment * kChunk + 16;
-  const int64_t row_bytes = kPacked ? len / 2 : len;
-  if (static_cast<int>(blockIdx.y) >= *a.active) return;
-  const MoeSlot& slot = a.slot[blockIdx.y];
-  const int e = slot.expert, count = slot.count;
-  if (tid < count) entries[tid] = slot.entry[tid];
-  const int64_t first = (static_cast<int64_t>(e) * rows + (lane & 15)) * row_bytes;
-  const uint8_t* const wide[2] = {(kGated ? a.gate : a.down) + first,
-                                  kGated ? a.up + first : a.down + first + 16 * row_bytes};
-  // Lanes of the last chunk's upper half may lie past the row: they read its first bytes
-  // and count as zeros.
+  const int row_bytes = kPacked ? len / 2 : len;
+  __shared__ SlotSearch::Shared shared;
+  SlotSearch search{a, shared};
+  MoeSlot& slot = a.slot[blockIdx.y];
+  int e, count;
+  if constexpr (kGated) {
+    e = search.find(blockIdx.y);
+    if (e < 0) return;
+  } else {
+    if (static_cast<int>(blockIdx.y) >= *a.active) return;
+    e = slot.expert, count = slot.count;
+    if (tid < count) entries[tid] = slot.entry[tid];
+  }
+  // Both strips of a tile's rows, in windows of the expert's matrices.
+  const int64_t first = static_cast<int64_t>(e) * rows * row_bytes;
+  const int size = rows * row_bytes, second = kGated ? 0 : 16 * row_bytes;
+  const few_rsrc wide[2] = {few_window((kGated ? a.gate : a.down) + first, size),
+                          few_window((kGated ? a.up : a.down) + first + second, size - second)};
+  // (lanes of the last chunk's upper half may lie past the row)
   const bool short_end = kPacked && (len & 127) != 0 && (lane & 32);
   const int mine = (chunks - ks + KS - 1) / KS;             // the wave's chunks ks, ks + KS, ...
   const int steps = (mine + kAhead - 1) / kAhead * kAhead;  // in whole rounds of the ring
   const int stride = gridDim.x * kTiles;
   v4i w[kAhead][2];
   auto load = [&](int tile, int i, v4i (&to)[2]) {
-    if (i < mine && tile < tiles) {
-      const int chunk = ks + i * KS;
-      const int64_t off = static_cast<int64_t>(tile) * kCols * row_bytes + chunk * 64 +
-                          (short_end && chunk == chunks - 1 ? 0 : 16 * g);
-      to[0] = load_v4i(wide[0] + off);
-      to[1] = load_v4i(wide[1] + off);
-    }
+    const int chunk = ks + i * KS, at = tile * kCols * row_bytes + (lane & 15) * row_bytes + chunk * 64 + 16 * g;
+    const bool none = i >= mine || tile >= tiles || (short_end && chunk == chunks - 1);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) to[p] = load_window(wide[p], none ? kNoBytes : at);
   };
   int tile = blockIdx.x * kTiles + wave / KS;
   auto begin = [&]() {
@@ -243,7 +187,15 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
     for (int i = 0; i < kAhead; ++i) load(tile, i, w[i]);
   };
   begin();
-  lds_sync();
+  if constexpr (kGated) {
+    count = search.collect(e, entries);
+    if (blockIdx.x == 0) {  // for the other product
+      if (tid == 0) slot.expert = e, slot.count = count;
+      if (tid < count) slot.entry[tid] = entries[tid];
+    }
+  } else {
+    lds_sync();
+  }
   for (int t0 = 0; t0 < count; t0 += 16 * T) {
     const int here = min(count - t0, 16 * T);
     // Codes of chunks segment s on, 32 columns a thread at a time; columns past the row as zeros.
@@ -286,10 +238,9 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
           for (int r = 0; r < kAhead; ++r) {
             const int i = i0 + r, chunk = ks + i * KS;
             if (i < mine && tile < tiles) {
-              const bool off = short_end && chunk == chunks - 1;
               v4i fw[2][F];
 #pragma unroll
-              for (int p = 0; p < 2; ++p) wide_frags<kPacked>(off ? v4i{} : w[r][p], fw[p]);
+              for (int p = 0; p < 2; ++p) wide_frags<kPacked>(w[r][p], fw[p]);
               const uint8_t* x = codes + (lane & 15) * pitch + (chunk - seg * segment) * kChunk + (kChunk / 4) * g;
 #pragma unroll
               for (int f = 0; f < F; ++f) {
@@ -304,10 +255,8 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
                 for (int p = 0; p < 2; ++p) s.wide[p] = mfma_i8(fw[p][f], ones_i8(), s.wide[p]);
               }
             }
-            if (i + kAhead < steps)
-              load(tile, i + kAhead, w[r]);
-            else
-              load(tile + stride, i + kAhead - steps, w[r]);
+            const bool next = i + kAhead >= steps;
+            load(next ? tile + stride : tile, next ? i + kAhead - steps : i + kAhead, w[r]);
           }
         }
       }
@@ -403,7 +352,7 @@ hipError_t launch_product(const MoeLaunch& a, int tiles, int chunks) {
   constexpr int kChunk = kFewChunk<kPacked>, kTiles = kWaves / KS;
   // All chunks at a time if they fit in LDS, else whole rounds of every wave's ring of loads.
   constexpr int kLds = 159 * 1024 - (KS > 1 ? kWaves * 2 * T * 1024 : 0);  // of 160 KB, beside the sums
-  constexpr int kFit = (kLds / (16 * T) - 16) / kChunk, kRound = 4 * KS, kMost = kFit / kRound * kRound;
+  constexpr int kFit = (kLds / (16 * T) - 16) / kChunk, kRound = kAhead * KS, kMost = kFit / kRound * kRound;
   static_assert(kMost >= kRound, "a segment holds a round");
   int segment = chunks;
   if (chunks > kFit) {
@@ -442,7 +391,10 @@ hipError_t launch_products(const MoeLaunch& a) {
 
 template <bool kPacked>
 hipError_t launch(const MoeLaunch& a, bool out_bf16) {
-  hipLaunchKernelGGL(quest_moe_route_kernel, dim3(1), dim3(64 * kRouteWaves), 0, a.stream, a);
+  const auto route = a.experts <= 64    ? quest_moe_route_kernel<1>
+                     : a.experts <= 128 ? quest_moe_route_kernel<2>
+                                        : quest_moe_route_kernel<kMoeMaxExperts / 64>;
+  hipLaunchKernelGGL(route, dim3(a.n), dim3(64), 0, a.stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   err = a.act == 0 ? launch_products<kPacked, 0>(a) : launch_products<kPacked, 1>(a);
@@ -473,6 +425,7 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
 }  // namespace
 
 hipError_t launch_moe(const MoeLaunch& a, bool packed, bool out_bf16) {
+  if (moe_is_few(a)) return launch_moe_few(a, packed, out_bf16);
   return packed ? launch<true>(a, out_bf16) : launch<false>(a, out_bf16);
 }
 

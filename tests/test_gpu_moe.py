@@ -197,3 +197,25 @@ def test_past_32_bit_offsets(dev):
     logits = torch.zeros(3, e, device=dev)
     logits[:, -1] = 5.0
     assert torch.equal(want, qa.moe_fwd(x, xs, 8, logits, *args, 4, 1))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("n", [1, 4])
+def test_few_tokens_with_some_experts_of_many(dev, n, packed):
+    """Of top_k = 32 as many as are not masked: 17, 9, 1 and 32."""
+    log(f"masked ranks n={n} packed={packed}")
+    logits = torch.randn((n, 40), generator=torch.Generator().manual_seed(15))
+    for t, found in enumerate((17, 9, 1)[:n]):
+        logits[t, found:] = -float("inf")
+    for over_all in (False, True):
+        run_case(dev, n, 40, 32, 192, 320, 8, 4, 8, 64, "gelu", packed, over_all, logits=logits)
+
+
+@pytest.mark.parametrize("n,top,m,e,packed", [(4, 8, 8192, 9, True), (3, 32, 2048, 33, False), (4, 9, 7296, 9, False),
+                                              (4, 1, 8192, 2, False), (2, 6, 1088, 129, True)])
+def test_few_tokens_as_among_many(dev, n, top, m, e, packed):
+    """A few tokens' outputs are those they have in a larger batch, at the widths where the form changes."""
+    log(f"few as many n={n} top={top} m={m}")
+    layer, x, xs, logits, y = run_case(dev, 7, e, top, 128, m, 8, 4, 8, 64, "silu", packed, seed=n + m)
+    few = layer(x[:n].clone(), xs[:n].clone(), 8, logits[:n].clone(), top, block=64, h_bits=8, out_dtype=torch.float32)
+    assert torch.equal(few, y[:n])
