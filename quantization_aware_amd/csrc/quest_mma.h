@@ -5,8 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace quest {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -92,20 +90,6 @@ __device__ __forceinline__ void tile_at(int pid, int tiles_m, int tiles_n, int& 
   const int gm = min(tiles_m - first_m, 8);
   tm = first_m + (pid % group) % gm;
   tn = (pid % group) / gm;
-}
-
-// Compute units of the current device (cached per device; concurrent first
-// calls on one device may both query it and store the same value).
-inline int device_cus() {
-  static std::atomic<int> cached[64] = {};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int cus = cached[dev].load(std::memory_order_relaxed);
-  if (cus == 0) {
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) cus = 256;
-    cached[dev].store(cus, std::memory_order_relaxed);
-  }
-  return cus;
 }
 
 }  // namespace quest

@@ -361,10 +361,16 @@ hipError_t launch_product(const MoeLaunch& a, int tiles, int chunks) {
   }
   const size_t lds = static_cast<size_t>(16 * T) * (segment * kChunk + 16);
   // Workgroups walk tiles, so that finding and bringing the tokens is paid once for
-  // several, down to about three workgroups a compute unit.
-  const int each = (tiles + kTiles - 1) / kTiles;
-  const int walk = static_cast<int>((static_cast<int64_t>(each) * a.slots + 767) / 768);
-  hipLaunchKernelGGL((quest_moe_product_kernel<kPacked, T, KS, kMode>), dim3((each + walk - 1) / walk, a.slots),
+  // several: at most two a compute unit, and as many as leave the fullest unit the fewest
+  // steps.  (64 tokens of 128 experts: gated in 256 workgroups 42.8 us, in 384 49.0, in 768
+  // 42.8; of 8 wide experts in 256 44.0, in 704 48.0.)
+  const int each = (tiles + kTiles - 1) / kTiles, cus = device_cus();
+  int wide = 1, least = 0x7FFFFFFF;
+  for (int w = 1; w <= each && (w == 1 || w * a.slots <= 2 * cus); ++w) {
+    const int steps = (w * a.slots + cus - 1) / cus * ((each + w - 1) / w);
+    if (steps <= least) wide = w, least = steps;
+  }
+  hipLaunchKernelGGL((quest_moe_product_kernel<kPacked, T, KS, kMode>), dim3(wide, a.slots),
                      dim3(64 * kWaves), lds, a.stream, a, segment);
   return hipGetLastError();
 }
