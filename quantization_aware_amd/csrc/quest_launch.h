@@ -291,8 +291,8 @@ struct MoeLaunch {
   hipStream_t stream;
 };
 hipError_t launch_moe(const MoeLaunch& a, bool packed, bool out_bf16);
-// Of it, the form for a few tokens, where it is the faster one.
-bool moe_is_few(const MoeLaunch& a);
+// Of it, the form for few tokens, and where it is the faster one.
+bool moe_is_few(const MoeLaunch& a, bool packed);
 hipError_t launch_moe_few(const MoeLaunch& a, bool packed, bool out_bf16);
 
 }  // namespace quest

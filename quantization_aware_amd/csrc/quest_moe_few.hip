@@ -1,4 +1,4 @@
-// The mixture-of-experts layer of quest_moe_fwd for one or a few tokens, in two kernels.
+// The mixture-of-experts layer of quest_moe_fwd for few tokens, in two kernels.
 //
 // With few tokens hardly two of them share an expert: each pair of a token and one of its
 // experts is taken by itself, and what the general form (quest_moe.hip) does in kernels
@@ -13,11 +13,13 @@
 // results are the same bits.
 //
 // What bounds it is latency: one token of top 8 of 64 experts of 2048 x 1024 at 4 bits
-// takes 8.0 + 9.4 us (the general form's five kernels 25.2), of which its 25 MB are 5.2 at
+// takes 8.1 + 8.0 us (the general form's five kernels 25.2), of which its 25 MB are 5.2 at
 // a copy's rate; two launches, the logits and then the weights behind them, and h and
 // then its transform are the rest.  Measured against it: all waves looking for the expert
 // themselves 17.5 together, 8 waves in gated 15.7 (but 33.4 instead of 30.8 for three
 // tokens), 16 in down 16.2 (but 33.2 instead of 29.6 for four), 8 chunks ahead 17.4.
+#include <cmath>
+
 #include "quest_few.h"
 #include "quest_i8.h"
 #include "quest_launch.h"
@@ -265,11 +267,21 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
 
 }  // namespace
 
-// In microseconds, this form and the general one: 4 tokens of top 8 of 64 experts of
-// 2048 x 1024 29.7 and 36.0, of top 2 of 8 of 2048 x 5632 47.8 and 58.4, of top 3 of 13 of
-// 704 x 448 9.5 and 18.1; 6 tokens 42.3 and 44.6, 68.3 and 64.4, 10.2 and 19.1; 8 tokens 51.7
-// and 47.0.  LDS holds the codes of a token's h.
-bool moe_is_few(const MoeLaunch& a) { return a.n <= 4 && a.top * a.m <= 1 << 16; }
+// This form reads an expert's weights again for each token that takes it, mostly from
+// caches, but spends some 10 us less on launches and what lies between the products.  It
+// pays as long as the bytes that are read again, for experts taken at random, stay below
+// some 40 MB: with this form and the general one, in us, 6 tokens of top 8 of 64 experts of
+// 2048 x 1024 at 4 bits (47 MB) 42.1 and 47.2, 8 (73 MB) 51.8 and 45.0; 16 of top 3 of 13 of
+// 704 x 448 at 8 bits (34 MB) 18.1 and 20.6, 32 (79 MB) 27.9 and 21.1; 8 of top 4 of 32 of
+// 1024 x 512 at 4 bits (9 MB) 14.7 and 21.9, 16 (28 MB) 24.7 and 22.4.  For up to 4 tokens, where
+// the general form's wide instructions are emptier still, below 100 MB: 4 of top 2 of 8 of
+// 2048 x 5632 at 8 bits (95 MB) 50.4 and 59.8.  LDS holds the codes of a token's h.
+bool moe_is_few(const MoeLaunch& a, bool packed) {
+  if (a.n > 32 || a.top * a.m > 1 << 16) return false;
+  const double pairs = a.n * a.top, experts = a.experts;
+  const double chosen = experts * (1.0 - std::pow(1.0 - 1.0 / experts, pairs));
+  return (pairs - chosen) * (3.0 * a.m * a.k) / (packed ? 2 : 1) <= (a.n <= 4 ? 100e6 : 40e6);
+}
 
 hipError_t launch_moe_few(const MoeLaunch& a, bool packed, bool out_bf16) {
   return packed ? launch<true>(a, out_bf16) : launch<false>(a, out_bf16);

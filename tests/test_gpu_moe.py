@@ -219,3 +219,38 @@ def test_few_tokens_as_among_many(dev, n, top, m, e, packed):
     layer, x, xs, logits, y = run_case(dev, 7, e, top, 128, m, 8, 4, 8, 64, "silu", packed, seed=n + m)
     few = layer(x[:n].clone(), xs[:n].clone(), 8, logits[:n].clone(), top, block=64, h_bits=8, out_dtype=torch.float32)
     assert torch.equal(few, y[:n])
+
+
+@pytest.mark.parametrize("n,e,top,k,m,xb,wb,hb,block,act,packed", [
+    # many tokens of few experts, few tokens of many, odd lengths and every type of code
+    (35, 1, 1, 64, 64, 8, 8, 8, 64, "silu", False),
+    (40, 64, 8, 256, 128, 4, 4, 4, 128, "silu", True),
+    (33, 256, 3, 128, 64, 8, 4, 8, 64, "gelu", True),
+    (47, 5, 5, 320, 192, 8, 8, 4, 64, "gelu", False),
+    (34, 130, 32, 128, 128, 5, 3, 6, 128, "silu", False),
+    (51, 70, 7, 192, 256, 8, 4, 8, 256, "silu", True),
+    (39, 13, 3, 704, 448, 6, 5, 6, 64, "gelu", False),
+    (64, 65, 8, 64, 64, 1, 1, 1, 64, "silu", False),
+    (48, 8, 2, 512, 320, 8, 4, 8, 64, "silu", True),
+    (36, 3, 2, 4160, 64, 8, 4, 8, 64, "silu", True),
+    (37, 2, 2, 64, 8192, 8, 4, 8, 256, "silu", True),
+    (64, 2, 2, 64, 8192, 8, 8, 8, 64, "gelu", False),
+    (1, 33, 32, 64, 2112, 8, 4, 8, 64, "silu", True),
+    (3, 9, 9, 64, 8192, 8, 4, 8, 128, "gelu", True),
+    (5, 12, 9, 128, 7424, 8, 8, 8, 256, "silu", False),
+])
+def test_larger_batches_and_layers(dev, n, e, top, k, m, xb, wb, hb, block, act, packed):
+    log(f"start n={n} e={e} top={top} {k}x{m} b={xb},{wb},{hb} block {block} {act} packed={packed}")
+    run_case(dev, n, e, top, k, m, xb, wb, hb, block, act, packed, n % 2 == 0, seed=n + e + k)
+
+
+@pytest.mark.parametrize("n,e,top,packed", [(33, 8, 2, True), (64, 24, 4, False)])
+def test_tokens_among_others(dev, n, e, top, packed):
+    """A token's output alone, in a few and in a full batch: the same bits."""
+    log(f"tokens among others n={n} e={e}")
+    layer, x, xs, logits, y = run_case(dev, n, e, top, 320, 192, 8, 4, 6, 64, "gelu", packed)
+    for first, count in ((0, 1), (5, 3), (n - 9, 9), (1, 32)):
+        rows = slice(first, first + count)
+        part = layer(x[rows].clone(), xs[rows].clone(), 8, logits[rows].clone(), top, block=64, h_bits=6, act="gelu",
+                     out_dtype=torch.float32)
+        assert torch.equal(part, y[rows])
