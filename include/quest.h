@@ -245,6 +245,16 @@ quest_status quest_trust_bwd(const void* grad, quest_dtype g_dtype, const uint8_
                              int block, void* grad_out, void* stream);
 
 /*
+ * The same of an fp32 gradient, rounded once, to bf16: for gradient products
+ * that come in fp32.
+ *   grad     device, rows*cols floats
+ *   grad_out device output, rows*cols bf16; must not overlap grad or mask
+ * The other arguments, pointers and errors are quest_trust_bwd's.
+ */
+quest_status quest_trust_bwd_narrow(const float* grad, const uint8_t* mask, int64_t rows, int64_t cols, int block,
+                                    void* grad_out, void* stream);
+
+/*
  * The matrix-core operand of a quantised tensor, for products of two of them
  * (quest_gemm).  The pages time QuEST's 4-bit matrix products against BF16
  * ones, quantisation, dequantisation and Hadamard costs included

@@ -42,6 +42,7 @@ __all__ = [
     "gated_fwd",
     "gated_bwd",
     "quantize_fwd_i8",
+    "trust_bwd_narrow",
     "dequantize_i8",
     "gemm_i8",
     "moe_fwd",
@@ -76,6 +77,7 @@ EXPORTED_SYMBOLS = (
     "quest_sparse24_index_bytes",
     "quest_dequantize",
     "quest_trust_bwd",
+    "quest_trust_bwd_narrow",
     "quest_codes_bytes",
     "quest_mask_bytes",
     "quest_act8_scale_bytes",
@@ -173,6 +175,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.quest_dequantize.restype = c_int
     lib.quest_trust_bwd.argtypes = [vp, c_int, vp, i64, i64, c_int, vp, vp]
     lib.quest_trust_bwd.restype = c_int
+    lib.quest_trust_bwd_narrow.argtypes = [vp, vp, i64, i64, c_int, vp, vp]
+    lib.quest_trust_bwd_narrow.restype = c_int
     lib.quest_codes_bytes.argtypes = [i64, i64, c_int]
     lib.quest_codes_bytes.restype = ctypes.c_size_t
     lib.quest_mask_bytes.argtypes = [i64, i64]
@@ -1011,6 +1015,23 @@ def quantize_fwd_i8(x: torch.Tensor, block: int, b: int, trust: float = 1.0, wit
 def _byte_codes(name: str, t) -> None:
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D int8 tensor (rows x cols)")
+
+
+def trust_bwd_narrow(grad: torch.Tensor, mask: torch.Tensor, block: int, out=None, stream=None) -> torch.Tensor:
+    """trust_bwd of a 2-D float32 gradient, rounded once, to bfloat16 (quest_trust_bwd_narrow)."""
+    if stream is not None:
+        with _on_stream(stream, grad):
+            return trust_bwd_narrow(grad, mask, block, out)
+    _matrix("grad", grad)
+    rows, cols = grad.shape
+    specs = (("grad", grad, torch.float32, None), ("mask", mask, torch.uint8, mask_bytes(rows, cols)))
+    if out is not None:
+        specs += (("out", out, torch.bfloat16, (rows, cols)),)
+    _check_tensors(grad.device, *specs)
+    if out is None:
+        out = torch.empty(rows, cols, dtype=torch.bfloat16, device=grad.device)
+    _launch("quest_trust_bwd_narrow", grad.device, grad.data_ptr(), mask.data_ptr(), rows, cols, int(block), out.data_ptr())
+    return out
 
 
 def dequantize_i8(codes: torch.Tensor, scale: torch.Tensor, b: int, out_dtype=torch.bfloat16, out=None,

@@ -731,6 +731,21 @@ quest_status quest_trust_bwd(const void* grad, quest_dtype g_dtype, const uint8_
                                           g_allow_mfma_bwd, static_cast<hipStream_t>(stream)));
 }
 
+quest_status quest_trust_bwd_narrow(const float* grad, const uint8_t* mask, int64_t rows, int64_t cols, int block,
+                                    void* grad_out, void* stream) {
+  const int lb = log2_block(block);
+  if (lb < 0) return QUEST_EUNSUPPORTED;
+  const quest_status sh = check_shape(rows, cols, block);
+  if (sh != QUEST_OK) return sh;
+  if (rows == 0) return QUEST_OK;
+  if (!grad || !mask || !grad_out) return QUEST_EINVAL;
+  const size_t n = static_cast<size_t>(rows * cols);
+  const Span spans[] = {{grad, 4 * n, false}, {mask, quest_mask_bytes(rows, cols), false}, {grad_out, 2 * n, true}};
+  const quest_status st = check_spans(spans, 3);
+  if (st != QUEST_OK) return st;
+  return from_hip(quest::launch_trust_bwd_narrow(grad, mask, rows, cols, lb, grad_out, static_cast<hipStream_t>(stream)));
+}
+
 size_t quest_act8_scale_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0 || rows > kMaxElements / cols) return 0;
   return static_cast<size_t>(rows) * static_cast<size_t>((cols + 31) / 32);

@@ -228,6 +228,8 @@ hipError_t launch_gated_bwd(const GatedBwdLaunch& a, bool bf16);
 // The forward that writes its codes as signed bytes (a.codes; a.mask may be
 // null), and the values of such codes.  cols a multiple of 64, up to 32768.
 hipError_t launch_fwd_i8(const void* x, int x_is_bf16, int log_block, int bits, const FwdLaunch& a);
+hipError_t launch_trust_bwd_narrow(const float* grad, const uint8_t* mask, int64_t rows, int64_t cols, int log_block,
+                                   void* grad_out, hipStream_t stream);
 hipError_t launch_dequantize_i8(const uint8_t* codes, const float* scale, int64_t rows, int64_t cols, int bits,
                                 void* out, int out_is_bf16, hipStream_t stream);
 

@@ -47,7 +47,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (dequantize, dequantize_i8, gemm, gemm_i8, quantize_fwd_ex, quantize_fwd_fp4, quantize_fwd_i8,
-               quantize_fwd_op, quantize_fwd_op_group, quantize_fwd_sparse24, trust_bwd)
+               quantize_fwd_op, quantize_fwd_op_group, quantize_fwd_sparse24, trust_bwd, trust_bwd_narrow)
 
 __all__ = ["QuestLinearFunction", "QuestLinearInt8Function", "quest_linear", "quest_linear_operand",
            "quest_linear_int8", "QuestLinear", "default_trust", "ONE_BIT_OUTER_TRUST", "GRIDS"]
@@ -239,20 +239,29 @@ class QuestLinearInt8Function(torch.autograd.Function):
             cx, sx, mx, cw, sw, mw = ctx.saved_tensors
         dtype = _product_dtype(compute_dtype)
         dy = dy.to(dtype).contiguous()
+        wide = {} if dtype == torch.float32 else {"out_dtype": torch.float32}
+
+        def masked(g, mask, to):
+            return trust_bwd_narrow(g, mask, block) if to == torch.bfloat16 else trust_bwd(g, mask, block, out=g)
+
+        # The products' sums stay in fp32 up to the gradients' own type: rounded to bf16 both before and after the
+        # transform, and Q before the product, the gradients were 0.0029 off instead of 0.0024 (a rounding is 0.0017).
         if ctx.joint and need_x and need_w:
             q = dequantize_i8(codes, scale, bits_x, out_dtype=dtype)
-            g = torch.empty((n + m, k), dtype=dtype, device=dy.device)
-            torch.mm(dy.t(), q[:n], out=g[n:])  # the weight's first, as in QuestLinearFunction
-            torch.mm(dy, q[n:], out=g[:n])
-            trust_bwd(g, mask, block, out=g)
-            return g[:n].to(ctx.dtypes[0]), g[n:].to(ctx.dtypes[1]), *(None,) * 7
+            g = torch.empty((n + m, k), dtype=torch.float32, device=dy.device)
+            torch.mm(dy.t(), q[:n], out=g[n:], **wide)  # the weight's first, as in QuestLinearFunction
+            torch.mm(dy, q[n:], out=g[:n], **wide)
+            if ctx.dtypes[0] == ctx.dtypes[1]:
+                d = masked(g, mask, ctx.dtypes[0])
+                return d[:n], d[n:], *(None,) * 7
+            return masked(g[:n], mx, ctx.dtypes[0]), masked(g[n:], mw, ctx.dtypes[1]), *(None,) * 7
         dx = dw = None
         if need_w:
-            g = torch.mm(dy.t(), dequantize_i8(cx, sx, bits_x, out_dtype=dtype))
-            dw = trust_bwd(g, mw, block, out=g).to(ctx.dtypes[1])
+            g = torch.mm(dy.t(), dequantize_i8(cx, sx, bits_x, out_dtype=dtype), **wide)
+            dw = masked(g, mw, ctx.dtypes[1])
         if need_x:
-            g = torch.mm(dy, dequantize_i8(cw, sw, bits_w, out_dtype=dtype))
-            dx = trust_bwd(g, mx, block, out=g).to(ctx.dtypes[0])
+            g = torch.mm(dy, dequantize_i8(cw, sw, bits_w, out_dtype=dtype), **wide)
+            dx = masked(g, mx, ctx.dtypes[0])
         return dx, dw, *(None,) * 7
 
 

@@ -192,3 +192,29 @@ def test_past_32_bit_offsets(dev):
     y = qa.gemm_i8(a, sa, 8, b, sb, 8)
     check_product(y[-300:, -300:], exact_product(a[-300:], sa[-300:], 8, b[-300:], sb[-300:], 8))
     check_product(y[33000:33100], exact_product(a[33000:33100], sa[33000:33100], 8, b, sb, 8))
+
+
+@pytest.mark.parametrize("rows,cols,block", [(1, 64, 64), (3, 256, 256), (37, 320, 64), (1000, 1152, 128), (5, 32768, 256)])
+def test_narrow_trust_backward(dev, rows, cols, block):
+    """fp32 gradients to bf16: H (M G) of the formula in 64 bits, and the fp32 form's values rounded once."""
+    log(f"narrow trust backward {rows}x{cols} block {block}")
+    g = torch.Generator().manual_seed(rows + cols)
+    grad = torch.randn(rows, cols, generator=g)
+    grad[0, :block] *= 1e30
+    mask = torch.randint(0, 256, (rows * cols // 8,), generator=g, dtype=torch.uint8)
+    buf = torch.full((rows + 2, cols), 7.0, dtype=torch.bfloat16, device=dev)
+    got = qa.trust_bwd_narrow(grad.to(dev), mask.to(dev), block, out=buf[:rows])
+    assert (buf[rows:] == 7.0).all()
+    assert torch.equal(got, qa.trust_bwd(grad.to(dev), mask.to(dev), block).to(torch.bfloat16))
+    keep = np.unpackbits(mask.numpy(), bitorder="little").reshape(rows, cols)
+    kept = (grad.double().numpy() * keep).reshape(rows, cols // block, block)
+    had = np.array([[1.0]])
+    while len(had) < block:
+        had = np.block([[had, had], [had, -had]])
+    want = (kept @ had / np.sqrt(block)).reshape(rows, cols)
+    # log2(block) additions and the factor, each half a step of fp32 of at most the sum of magnitudes; then bf16's
+    size = np.abs(kept).sum(-1, keepdims=True) / np.sqrt(block) * np.ones(block)
+    bound = 2.0 ** -8 * np.abs(want) + 12 * U * size.reshape(rows, cols) * (1 + 2.0 ** -8)
+    assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+    assert torch.equal(got, qa.trust_bwd_narrow(grad.to(dev), mask.to(dev), block))
+    assert qa.trust_bwd_narrow(grad[:0].to(dev), mask[:0].to(dev), block).shape == (0, cols)

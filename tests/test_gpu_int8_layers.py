@@ -290,3 +290,39 @@ def test_frozen_product_call(dev):
     y = quest_linear_int8(x, codes, scale, 5, bias=torch.ones(72, device=dev), block=64, bits_x=7, out_dtype=torch.float32)
     cx, sx, _ = qa.quantize_fwd_i8(x.reshape(12, 256), 64, 7)
     assert torch.equal(y.reshape(12, 72), qa.gemm_i8(cx, sx, 7, codes, scale, 5, out_dtype=torch.float32) + 1.0)
+
+
+@pytest.mark.parametrize("x_dtype,w_dtype,compute", [
+    (torch.bfloat16, torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32, torch.bfloat16),
+    (torch.float32, torch.bfloat16, torch.float32), (torch.float32, torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("n,bits_w", [(64, 8), (7, 6), (0, 8)])
+def test_gradients_of_each_type(dev, x_dtype, w_dtype, compute, n, bits_w):
+    """Gradients come in their tensors' types, those in fp32 without a rounding to bf16 on the way."""
+    log(f"gradient types n={n} bits {bits_w} {x_dtype} {w_dtype} {compute}")
+    gen = torch.Generator().manual_seed(n)
+    x = torch.randn(n, 256, generator=gen).to(dev, x_dtype).requires_grad_()
+    w = torch.randn(96, 256, generator=gen).to(dev, w_dtype).requires_grad_()
+    dy = torch.randn(n, 96, generator=gen).to(dev, compute)
+    y = quest_linear(x, w, bits_x=8, bits_w=bits_w, compute_dtype=compute, int8=True)
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    assert dx.dtype == x_dtype and dw.dtype == w_dtype and dx.shape == x.shape and dw.shape == w.shape
+    if not n:
+        assert (dw == 0).all()
+        return
+    qs = []
+    for t, b in ((x, 8), (w, bits_w)):
+        c, s, m = qa.quantize_fwd_i8(t.detach(), 128, b, with_mask=True)
+        qs.append((qa.dequantize_i8(c, s, b, out_dtype=compute).double(), m))
+    # In 64 bits from the values that are multiplied; the products' fp32 sums of n or 96 terms and the transform's
+    # seven additions and factor are off by at most so many steps of the sum of magnitudes.
+    for got, g, size, m in ((dx, dy.double() @ qs[1][0], dy.double().abs() @ qs[1][0].abs(), qs[0][1]),
+                            (dw, dy.double().t() @ qs[0][0], dy.double().abs().t() @ qs[0][0].abs(), qs[1][1])):
+        shifts = torch.arange(8, dtype=torch.uint8, device=dev)
+        keep = ((m.reshape(-1, 1) >> shifts) & 1).reshape(g.shape).double()
+        had = torch.ones(1, 1, dtype=torch.float64, device=dev)
+        while len(had) < 128:
+            had = torch.cat([torch.cat([had, had], 1), torch.cat([had, -had], 1)])
+        want = ((g * keep).reshape(-1, 128) @ had / 128 ** 0.5).reshape(g.shape)
+        most = (size.reshape(-1, 128).sum(-1, keepdim=True) / 128 ** 0.5).expand(-1, 128).reshape(g.shape)
+        eps = torch.finfo(got.dtype).eps / 2
+        assert ((got.double() - want).abs() <= eps * want.abs() + (max(n, 96) + 9) * 2.0 ** -24 * most * (1 + eps)).all()

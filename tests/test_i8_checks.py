@@ -118,6 +118,17 @@ def test_experts_reject(lib, kw, status):
     assert moe(lib, **kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(block=32), EUNSUPPORTED), (dict(rows=-1), EINVAL), (dict(cols=200), EINVAL), (dict(cols=0), EINVAL),
+    (dict(cols=1 << 25), EUNSUPPORTED), (dict(rows=1 << 40), EUNSUPPORTED), (dict(grad=None), EINVAL), (dict(mask=None), EINVAL),
+    (dict(out=None), EINVAL), (dict(grad=P[0] + 4), EALIGN), (dict(mask=P[1] + 8), EALIGN), (dict(out=P[2] + 2), EALIGN),
+    (dict(out=P[0]), EINVAL), (dict(out=P[1] - 16), EINVAL), (dict(rows=0, grad=None, mask=None, out=None), OK),
+])
+def test_narrow_trust_backward_rejects(lib, kw, status):
+    a = dict(dict(grad=P[0], mask=P[1], rows=4, cols=256, block=128, out=P[2]), **kw)
+    assert lib.quest_trust_bwd_narrow(*a.values(), None) == status
+
+
 def test_workspace_bytes(lib):
     f = lib.quest_moe_workspace_bytes
     # h and the products in fp32, h's codes; a slot (144 bytes) and three words for each row
@@ -145,6 +156,11 @@ def test_workspace_bytes(lib):
     (lambda: qa.dequantize_i8(i8(4, 256), t(3), 8), ValueError, "scale must have shape"),
     (lambda: qa.dequantize_i8(i8(4, 256), t(4), 8, out=t(4, 255)), ValueError, "out must have shape"),
     (lambda: qa.dequantize_i8(i8(4, 256), t(4), 8, out_dtype=torch.float16), TypeError, "float32 or bfloat16"),
+    (lambda: qa.trust_bwd_narrow(t(256), t(32, dtype=torch.uint8), 128), ValueError, "2-D"),
+    (lambda: qa.trust_bwd_narrow(t(4, 256, dtype=torch.bfloat16), t(128, dtype=torch.uint8), 128), TypeError, "grad must be"),
+    (lambda: qa.trust_bwd_narrow(t(4, 256), t(127, dtype=torch.uint8), 128), ValueError, "mask"),
+    (lambda: qa.trust_bwd_narrow(t(4, 256), t(128, dtype=torch.uint8), 128, out=t(4, 256)), TypeError, "out must be"),
+    (lambda: qa.trust_bwd_narrow(t(4, 256), t(128, dtype=torch.uint8), 128), ValueError, "GPU tensor"),
     (lambda: qa.gemm_i8(i8(256), t(4), 8, i8(5, 256), t(5), 8), ValueError, "a must be a 2-D"),
     (lambda: qa.gemm_i8(i8(4, 256), t(4), 8, i8(5), t(5), 8), ValueError, "b must be a 2-D"),
     (lambda: qa.gemm_i8(t(4, 256), t(4), 8, i8(5, 256), t(5), 8), TypeError, "a must be"),
