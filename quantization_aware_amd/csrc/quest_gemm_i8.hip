@@ -11,6 +11,17 @@
 // up to.  The roundings are those of quest_gemm: 2 / (2^b - 1) and D for both
 // operands, D_a D_b, T to fp32, the product, and the output type.  Where
 // |T| < 2^24 both products give the same bits.
+//
+// Large products are bound by the matrix cores, and there by power: 16384 x 2048 -> 5632
+// takes 200 to 216 us, 1.75 to 1.9 POP/s (a library's product of the same codes to int32,
+// without scales, 215; instructions alone on such data 3.5 POP/s, on zeros 4.5).  What is
+// between: writing the 185 MB of outputs (some 50 us of it without the epilogue), the
+// loads (40 without them) and the row sums (2 to 12).  Sums by dot products after the
+// four products of a part, not between them: there they stall the matrix cores (+ 26 us).
+// Outputs written through the L2 (sc0 sc1) leave it to the operands: 17 us less than
+// plain stores; non-temporal ones gain 14 here and lose 9 at 16384 x 2048 -> 2048.
+// 2048 x 5632 -> 2048 takes 30.4 us, 4096 x 2048 -> 5632 54, 333 x 960 -> 1001 to fp32 4.7,
+// 48 x 2048 -> 5632 6.5 and one row 2048 -> 2048 3.1 us: the last three are latency.
 #include <type_traits>
 
 #include "quest_few.h"
@@ -127,165 +138,165 @@ __device__ __forceinline__ void i8_tile(const GemmI8Launch& g, int row0, int col
   each_buffer([&](auto i) {
     if constexpr (decltype(i)::value < NB - 1) fetch(decltype(i)::value, i);
   });
-    v16i acc[JB][IB];
+  v16i acc[JB][IB];
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+  for (int j = 0; j < JB; ++j)
 #pragma unroll
-      for (int i = 0; i < IB; ++i) acc[j][i] = v16i{};
-    v4i sum_a[kSumA] = {}, sum_b[kSumB] = {};  // (four each: a chain of them would wait for itself)
-    renew();
-    int lane_off[4];
+    for (int i = 0; i < IB; ++i) acc[j][i] = v16i{};
+  v4i sum_a[kSumA] = {}, sum_b[kSumB] = {};  // (four each: a chain of them would wait for itself)
+  renew();
+  int lane_off[4];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const int r32 = lane & 31, h = lane >> 5;
-      lane_off[ks] = r32 * kStageK + 16 * ((2 * ks + h) ^ swizzle(r32));
-    }
-    auto frag = [&](auto bi, int op, int blk, int ks) -> v4i {
-      return *reinterpret_cast<const v4i*>(stage_mem(bi) + op * kStageA + blk * (32 * kStageK) + lane_off[ks]);
-    };
-    v4i f0a[IB], f0b[JB], f1a[IB], f1b[JB];
-    auto read = [&](auto bi, int ks, v4i (&fa)[IB], v4i (&fb)[JB]) {
-#pragma unroll
-      for (int i = 0; i < IB; ++i) fa[i] = frag(bi, 0, row_block(i), ks);
-#pragma unroll
-      for (int j = 0; j < JB; ++j) fb[j] = frag(bi, 1, col_block(j), ks);
-    };
-    auto multiply = [&](const v4i (&fa)[IB], const v4i (&fb)[JB]) {
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int j = 0; j < JB; ++j)
-#pragma unroll
-        for (int i = 0; i < IB; ++i)
-          acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[j][i], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-#pragma unroll
-        for (int i = 0; i < kSumA; ++i) sum_a[i][d] = __builtin_amdgcn_sdot4(fa[i][d], 0x01010101, sum_a[i][d], false);
-#pragma unroll
-        for (int j = 0; j < kSumB; ++j) sum_b[j][d] = __builtin_amdgcn_sdot4(fb[j][d], 0x01010101, sum_b[j][d], false);
-      }
-    };
-    constexpr int kInFlight = (NB - 2) * kLoads;
-    wait_vmcnt<kInFlight>();  // stage 0 has landed
-    lds_barrier();
-    read(std::integral_constant<int, 0>{}, 0, f0a, f0b);
-    // Step s lies in buffer i; the one before i held s - 1, whose reads every wave
-    // finished before the last barrier, and receives s + NB - 1.  A step's products come
-    // in four parts, each while the next one's fragments are read.
-    auto step = [&](int s, auto i) {
-      constexpr int I = decltype(i)::value;
-      fetch(s + NB - 1, index(std::integral_constant<int, I + NB - 1>{}));
-      read(i, 1, f1a, f1b);
-      multiply(f0a, f0b);
-      read(i, 2, f0a, f0b);
-      multiply(f1a, f1b);
-      read(i, 3, f1a, f1b);
-      multiply(f0a, f0b);
-      wait_vmcnt<kInFlight>();  // step s + 1's stage has landed
-      lds_barrier();            // for every wave, and all reads of this one are done
-      read(index(std::integral_constant<int, I + 1>{}), 0, f0a, f0b);
-      multiply(f1a, f1b);
-    };
-    int s = 0;
-    for (; s + NB <= stages; s += NB) each_buffer([&](auto i) { step(s + decltype(i)::value, i); });
-    const int left = stages - s;
-    each_buffer([&](auto i) {
-      if (decltype(i)::value < left) step(s + decltype(i)::value, i);
-    });
-
-    // The row sums (both halves of a wave hold one each) to where every wave finds them.
-    renew();
+  for (int ks = 0; ks < 4; ++ks) {
     const int r32 = lane & 31, h = lane >> 5;
+    lane_off[ks] = r32 * kStageK + 16 * ((2 * ks + h) ^ swizzle(r32));
+  }
+  auto frag = [&](auto bi, int op, int blk, int ks) -> v4i {
+    return *reinterpret_cast<const v4i*>(stage_mem(bi) + op * kStageA + blk * (32 * kStageK) + lane_off[ks]);
+  };
+  v4i f0a[IB], f0b[JB], f1a[IB], f1b[JB];
+  auto read = [&](auto bi, int ks, v4i (&fa)[IB], v4i (&fb)[JB]) {
 #pragma unroll
-    for (int i = 0; i < kSumA; ++i) {
-      int v = sum_a[i][0] + sum_a[i][1] + sum_a[i][2] + sum_a[i][3];
-      v += __shfl_xor(v, 32);
-      if (kSumA * wn < IB && h == 0) sums[32 * row_block(i) + r32] = v;
-    }
+    for (int i = 0; i < IB; ++i) fa[i] = frag(bi, 0, row_block(i), ks);
 #pragma unroll
-    for (int j = 0; j < kSumB; ++j) {
-      int v = sum_b[j][0] + sum_b[j][1] + sum_b[j][2] + sum_b[j][3];
-      v += __shfl_xor(v, 32);
-      if (kSumB * wm < JB && h == 1) sums[kTileM + 32 * col_block(j) + r32] = v;
-    }
-    lds_barrier();
-    // A wave's column factors and sums: 16 columns a lane of each block of 32.
-    float fb[JB][16];
-    uint32_t tb[JB][16];
+    for (int j = 0; j < JB; ++j) fb[j] = frag(bi, 1, col_block(j), ks);
+  };
+  auto multiply = [&](const v4i (&fa)[IB], const v4i (&fb)[JB]) {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int j = 0; j < JB; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = kTileM + 32 * col_block(j) + 8 * q + 4 * h;
-        const float4 f = *reinterpret_cast<const float4*>(&fac[c]);
-        const int4 t = *reinterpret_cast<const int4*>(&sums[c]);
-        fb[j][4 * q] = f.x * g.kb, fb[j][4 * q + 1] = f.y * g.kb, fb[j][4 * q + 2] = f.z * g.kb;
-        fb[j][4 * q + 3] = f.w * g.kb;
-        tb[j][4 * q] = 2u * t.x, tb[j][4 * q + 1] = 2u * t.y, tb[j][4 * q + 2] = 2u * t.z, tb[j][4 * q + 3] = 2u * t.w;
+      for (int i = 0; i < IB; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[j][i], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+#pragma unroll
+      for (int i = 0; i < kSumA; ++i) sum_a[i][d] = __builtin_amdgcn_sdot4(fa[i][d], 0x01010101, sum_a[i][d], false);
+#pragma unroll
+      for (int j = 0; j < kSumB; ++j) sum_b[j][d] = __builtin_amdgcn_sdot4(fb[j][d], 0x01010101, sum_b[j][d], false);
+    }
+  };
+  constexpr int kInFlight = (NB - 2) * kLoads;
+  wait_vmcnt<kInFlight>();  // stage 0 has landed
+  lds_barrier();
+  read(std::integral_constant<int, 0>{}, 0, f0a, f0b);
+  // Step s lies in buffer i; the one before i held s - 1, whose reads every wave
+  // finished before the last barrier, and receives s + NB - 1.  A step's products come
+  // in four parts, each while the next one's fragments are read.
+  auto step = [&](int s, auto i) {
+    constexpr int I = decltype(i)::value;
+    fetch(s + NB - 1, index(std::integral_constant<int, I + NB - 1>{}));
+    read(i, 1, f1a, f1b);
+    multiply(f0a, f0b);
+    read(i, 2, f0a, f0b);
+    multiply(f1a, f1b);
+    read(i, 3, f1a, f1b);
+    multiply(f0a, f0b);
+    wait_vmcnt<kInFlight>();  // step s + 1's stage has landed
+    lds_barrier();            // for every wave, and all reads of this one are done
+    read(index(std::integral_constant<int, I + 1>{}), 0, f0a, f0b);
+    multiply(f1a, f1b);
+  };
+  int s = 0;
+  for (; s + NB <= stages; s += NB) each_buffer([&](auto i) { step(s + decltype(i)::value, i); });
+  const int left = stages - s;
+  each_buffer([&](auto i) {
+    if (decltype(i)::value < left) step(s + decltype(i)::value, i);
+  });
+
+  // The row sums (both halves of a wave hold one each) to where every wave finds them.
+  renew();
+  const int r32 = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < kSumA; ++i) {
+    int v = sum_a[i][0] + sum_a[i][1] + sum_a[i][2] + sum_a[i][3];
+    v += __shfl_xor(v, 32);
+    if (kSumA * wn < IB && h == 0) sums[32 * row_block(i) + r32] = v;
+  }
+#pragma unroll
+  for (int j = 0; j < kSumB; ++j) {
+    int v = sum_b[j][0] + sum_b[j][1] + sum_b[j][2] + sum_b[j][3];
+    v += __shfl_xor(v, 32);
+    if (kSumB * wm < JB && h == 1) sums[kTileM + 32 * col_block(j) + r32] = v;
+  }
+  lds_barrier();
+  // A wave's column factors and sums: 16 columns a lane of each block of 32.
+  float fb[JB][16];
+  uint32_t tb[JB][16];
+#pragma unroll
+  for (int j = 0; j < JB; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = kTileM + 32 * col_block(j) + 8 * q + 4 * h;
+      const float4 f = *reinterpret_cast<const float4*>(&fac[c]);
+      const int4 t = *reinterpret_cast<const int4*>(&sums[c]);
+      fb[j][4 * q] = f.x * g.kb, fb[j][4 * q + 1] = f.y * g.kb, fb[j][4 * q + 2] = f.z * g.kb;
+      fb[j][4 * q + 3] = f.w * g.kb;
+      tb[j][4 * q] = 2u * t.x, tb[j][4 * q + 1] = 2u * t.y, tb[j][4 * q + 2] = 2u * t.z, tb[j][4 * q + 3] = 2u * t.w;
+    }
+  const auto rout = make_rsrc(static_cast<Out*>(g.out) + static_cast<size_t>(row0) * n,
+                              static_cast<uint32_t>(min(m - row0, kTileM)) * static_cast<uint32_t>(n) * kOut);
+#pragma unroll
+  for (int i = 0; i < IB; ++i) {
+    const int rr = 32 * row_block(i) + r32;
+    const float fa = fac[rr] * g.ka;
+    const uint32_t ta = 2u * static_cast<uint32_t>(sums[rr]) + static_cast<uint32_t>(k);
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        // (unsigned: the terms may wrap, their sum does not; g.ka holds the quarter)
+        const uint32_t v = 4u * static_cast<uint32_t>(acc[j][i][e]) + (tb[j][e] + ta);
+        y[e] = static_cast<float>(static_cast<int>(v)) * (fa * fb[j][e]);
       }
-    const auto rout = make_rsrc(static_cast<Out*>(g.out) + static_cast<size_t>(row0) * n,
-                                static_cast<uint32_t>(min(m - row0, kTileM)) * static_cast<uint32_t>(n) * kOut);
+      // Whole 64-byte pieces of rows: a lane has four columns of every eight; the lane
+      // 16 away, and for bf16 first the one 32 away, trade them for neighbouring ones.
+      // Then chunk c of lane l is row 16 c' + l % 16, c' and the column from its place.
+      constexpr int kDwords = 4 * kOut;
+      uint32_t w[kDwords];
+      if constexpr (kOut == 4) {
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
-      const int rr = 32 * row_block(i) + r32;
-      const float fa = fac[rr] * g.ka;
-      const uint32_t ta = 2u * static_cast<uint32_t>(sums[rr]) + static_cast<uint32_t>(k);
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        float y[16];
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
+        // quad q's dwords 2 q, 2 q + 1: the halves trade quads 0, 2 and 1, 3
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          // (unsigned: the terms may wrap, their sum does not; g.ka holds the quarter)
-          const uint32_t v = 4u * static_cast<uint32_t>(acc[j][i][e]) + (tb[j][e] + ta);
-          y[e] = static_cast<float>(static_cast<int>(v)) * (fa * fb[j][e]);
+        for (int d = 0; d < 4; ++d) {
+          const auto s2 = __builtin_amdgcn_permlane32_swap(w[d], w[d + 4], false, false);
+          w[d] = s2[0], w[d + 4] = s2[1];
         }
-        // Whole 64-byte pieces of rows: a lane has four columns of every eight; the lane
-        // 16 away, and for bf16 first the one 32 away, trade them for neighbouring ones.
-        // Then chunk c of lane l is row 16 c' + l % 16, c' and the column from its place.
-        constexpr int kDwords = 4 * kOut;
-        uint32_t w[kDwords];
-        if constexpr (kOut == 4) {
+        // lane half h: columns 16 h .. + 15 in the order of dwords 0 1 4 5 2 3 6 7
+        const uint32_t x2 = w[2], x3 = w[3];
+        w[2] = w[4], w[3] = w[5], w[4] = x2, w[5] = x3;
+      }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e]);
-        } else {
+      for (int p = 0; p < kDwords / 8; ++p) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
-          // quad q's dwords 2 q, 2 q + 1: the halves trade quads 0, 2 and 1, 3
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const auto s2 = __builtin_amdgcn_permlane32_swap(w[d], w[d + 4], false, false);
-            w[d] = s2[0], w[d + 4] = s2[1];
-          }
-          // lane half h: columns 16 h .. + 15 in the order of dwords 0 1 4 5 2 3 6 7
-          const uint32_t x2 = w[2], x3 = w[3];
-          w[2] = w[4], w[3] = w[5], w[4] = x2, w[5] = x3;
+        for (int d = 0; d < 4; ++d) {
+          const auto s2 = __builtin_amdgcn_permlane16_swap(w[8 * p + d], w[8 * p + 4 + d], false, false);
+          w[8 * p + d] = s2[0], w[8 * p + 4 + d] = s2[1];
         }
 #pragma unroll
-        for (int p = 0; p < kDwords / 8; ++p) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const auto s2 = __builtin_amdgcn_permlane16_swap(w[8 * p + d], w[8 * p + 4 + d], false, false);
-            w[8 * p + d] = s2[0], w[8 * p + 4 + d] = s2[1];
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int row = 32 * row_block(i) + 16 * c + (lane & 15);
-            // fp32: 32 bytes of quad 2 p + (l / 16) % 2; bf16: the half's 8-column pieces
-            const int cl = kOut == 4 ? 8 * (2 * p + ((lane >> 4) & 1)) + 4 * h : 16 * h + 8 * ((lane >> 4) & 1);
-            const int col = col0 + 32 * col_block(j) + cl;
-            const u32x4 chunk = {w[8 * p + 4 * c], w[8 * p + 4 * c + 1], w[8 * p + 4 * c + 2], w[8 * p + 4 * c + 3]};
-            if constexpr (kVec) {
-              // n is a multiple of kPer: a chunk is wholly inside or wholly past the row
-              const int off = col < n ? (row * n + col) * kOut : kNowhereOff;
-              __builtin_amdgcn_raw_buffer_store_b128(chunk, rout, off, 0, kWriteThrough);
-            } else if (row0 + row < m && col < n) {
-              store_part(static_cast<Out*>(g.out) + static_cast<int64_t>(row0 + row) * n + col, chunk, n - col);
-            }
+        for (int c = 0; c < 2; ++c) {
+          const int row = 32 * row_block(i) + 16 * c + (lane & 15);
+          // fp32: 32 bytes of quad 2 p + (l / 16) % 2; bf16: the half's 8-column pieces
+          const int cl = kOut == 4 ? 8 * (2 * p + ((lane >> 4) & 1)) + 4 * h : 16 * h + 8 * ((lane >> 4) & 1);
+          const int col = col0 + 32 * col_block(j) + cl;
+          const u32x4 chunk = {w[8 * p + 4 * c], w[8 * p + 4 * c + 1], w[8 * p + 4 * c + 2], w[8 * p + 4 * c + 3]};
+          if constexpr (kVec) {
+            // n is a multiple of kPer: a chunk is wholly inside or wholly past the row
+            const int off = col < n ? (row * n + col) * kOut : kNowhereOff;
+            __builtin_amdgcn_raw_buffer_store_b128(chunk, rout, off, 0, kWriteThrough);
+          } else if (row0 + row < m && col < n) {
+            store_part(static_cast<Out*>(g.out) + static_cast<int64_t>(row0 + row) * n + col, chunk, n - col);
           }
         }
       }
     }
+  }
 }
 
 // Workgroups are dealt to the 8 XCDs round-robin; each XCD takes a contiguous range of

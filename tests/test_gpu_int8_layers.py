@@ -326,3 +326,9 @@ def test_gradients_of_each_type(dev, x_dtype, w_dtype, compute, n, bits_w):
         most = (size.reshape(-1, 128).sum(-1, keepdim=True) / 128 ** 0.5).expand(-1, 128).reshape(g.shape)
         eps = torch.finfo(got.dtype).eps / 2
         assert ((got.double() - want).abs() <= eps * want.abs() + (max(n, 96) + 9) * 2.0 ** -24 * most * (1 + eps)).all()
+
+
+def test_no_tokens(dev):
+    layer = QuestMoE(128, 128, 4, 2, device=dev, dtype=torch.bfloat16)
+    assert layer(torch.zeros(0, 128, dtype=torch.bfloat16, device=dev)).shape == (0, 128)
+    assert layer.freeze()(torch.zeros(2, 0, 128, dtype=torch.bfloat16, device=dev)).shape == (2, 0, 128)

@@ -254,3 +254,38 @@ def test_tokens_among_others(dev, n, e, top, packed):
         part = layer(x[rows].clone(), xs[rows].clone(), 8, logits[rows].clone(), top, block=64, h_bits=6, act="gelu",
                      out_dtype=torch.float32)
         assert torch.equal(part, y[rows])
+
+
+def test_past_32_bit_offsets_of_many_tokens(dev):
+    """Weights of more than 2^32 bytes in a batch whose tokens share experts."""
+    e, k, m, n = 40, 32768, 4096, 40
+    log("experts of 5 GB, many tokens")
+    g = torch.Generator().manual_seed(16)
+    alone = []
+    for shape in ((m, k), (m, k), (k, m)):
+        c, s = coded(shape, 4, g)
+        u = (c + 8).to(torch.uint8)
+        alone += [(u[:, 0::2] | (u[:, 1::2] << 4)).to(dev)[None].contiguous(), s.to(dev)[None].contiguous()]
+    x, xs, _ = tokens(dev, n, k, 8, 17)
+    want = qa.moe_fwd(x, xs, 8, torch.zeros(n, 1, device=dev), *alone, 4, 1)
+    args = []
+    for t in alone:
+        wide = torch.zeros((e, *t.shape[1:]), dtype=t.dtype, device=dev)
+        wide[-1] = t[0]
+        args.append(wide)
+    logits = torch.zeros(n, e, device=dev)
+    logits[:, -1] = 5.0
+    assert torch.equal(want, qa.moe_fwd(x, xs, 8, logits, *args, 4, 1))
+
+
+def test_on_a_stream_of_its_own(dev):
+    """Calls with stream=, a few and many tokens at once on two streams, and no others waiting for them."""
+    layer = Layer(dev, 16, 512, 256, 4, True, 18)
+    sets = [tokens(dev, n, 512, 8, 19 + n)[:2] + (torch.randn(n, 16, device=dev),) for n in (2, 50)]
+    want = [layer(x, xs, 8, logits, 4) for x, xs, logits in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[layer(x, xs, 8, logits, 4, stream=s) for (x, xs, logits), s in zip(sets, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(a, b) for a, b in zip(pair, want))
