@@ -7,7 +7,6 @@
 
 namespace quest {
 
-
 // A workgroup barrier that waits for this wave's LDS accesses only: loads of weights
 // stay in flight across it (a __syncthreads waits for them).
 __device__ __forceinline__ void lds_sync() {
@@ -18,7 +17,7 @@ __device__ __forceinline__ void lds_sync() {
 }
 
 // A token's logits as they lie in memory, expert 64 i + lane in raw[i] (past the last:
-// the last again).  Kept apart from their use, so that several tokens' loads overlap.
+// the last again).  Kept apart from their use, so that other loads can follow at once.
 template <int S>
 __device__ __forceinline__ void fetch_logits(const MoeLaunch& a, int t, int lane, uint32_t (&raw)[S]) {
   const int64_t row = static_cast<int64_t>(t) * a.experts;
