@@ -20,7 +20,8 @@
 // four products of a part, not between them: there they stall the matrix cores (+ 26 us).
 // Outputs written through the L2 (sc0 sc1) leave it to the operands: 17 us less than
 // plain stores; non-temporal ones gain 14 here and lose 9 at 16384 x 2048 -> 2048.
-// 2048 x 5632 -> 2048 takes 30.4 us, 4096 x 2048 -> 5632 54, 333 x 960 -> 1001 to fp32 4.7,
+// 2048 x 5632 -> 2048 takes 30.4 us (its 256 tiles read 12 TB/s from the L2; 4 waves of
+// 64 x 64 each instead of 8, or three stages, change nothing), 4096 x 2048 -> 5632 54, 333 x 960 -> 1001 to fp32 4.7,
 // 48 x 2048 -> 5632 6.5 and one row 2048 -> 2048 3.1 us: the last three are latency.
 #include <type_traits>
 
