@@ -1134,7 +1134,7 @@ def moe_fwd(x: torch.Tensor, x_scale: torch.Tensor, x_bits: int, logits: torch.T
     _check_tensors(dev, *specs)
     if out is None:
         out = torch.empty(n, k, dtype=out_dtype, device=dev)
-    need = min(n, MOE_MAX_TOKENS) * top_k * (4 * k + 5 * m + 156) + 64  # quest_moe_workspace_bytes
+    need = min(n, MOE_MAX_TOKENS) * top_k * (4 * k + 5 * m + 156)  # quest_moe_workspace_bytes
     ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     _launch("quest_moe_fwd", dev, x.data_ptr(), x_scale.data_ptr(), n, int(x_bits), logits.data_ptr(), logits_code,
             experts, top_k, int(over_all), gate.data_ptr(), gate_scale.data_ptr(), up.data_ptr(), up_scale.data_ptr(),

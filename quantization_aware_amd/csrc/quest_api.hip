@@ -542,8 +542,8 @@ size_t quest_moe_workspace_bytes(int64_t n, int64_t top_k, int64_t k, int64_t m)
       m <= 0 || m > quest::kMoeMaxWidth)
     return 0;
   // a row for each token and rank: h and the products in fp32, h's codes, a slot, h's clip scale, a
-  // weight and a count; and the number of slots
-  return static_cast<size_t>(n * top_k) * (static_cast<size_t>(4 * k + 5 * m) + sizeof(quest::MoeSlot) + 12) + 64;
+  // weight and a count
+  return static_cast<size_t>(n * top_k) * (static_cast<size_t>(4 * k + 5 * m) + sizeof(quest::MoeSlot) + 12);
 }
 
 quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int x_bits, const void* logits,
@@ -610,8 +610,7 @@ quest_status quest_moe_fwd(const int8_t* x, const float* x_scale, int64_t n, int
   a.y = a.h + rows * m;
   a.hc = reinterpret_cast<uint8_t*>(a.y + rows * k);
   a.slot = reinterpret_cast<quest::MoeSlot*>(a.hc + rows * m);
-  a.active = reinterpret_cast<int*>(a.slot + rows);
-  a.hs = reinterpret_cast<float*>(a.active + 16);
+  a.hs = reinterpret_cast<float*>(a.slot + rows);
   a.weight = a.hs + rows;
   a.found = reinterpret_cast<int*>(a.weight + rows);
   a.out = out;

@@ -254,7 +254,7 @@ hipError_t launch_gemm_i8(const GemmI8Launch& g, bool out_bf16);
 // signed byte codes (experts x m x k, down experts x k x m), or packed 4-bit ones.
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTop = 32, kMoeMaxWidth = 8192;
 struct MoeSlot {  // a chosen expert and its tokens: token | rank of the expert among the token's << 8
-  int expert, count;
+  int expert, count;  // expert -1: none
   uint16_t entry[kMoeMaxTokens];
   int unused[2];  // (to a multiple of 16 bytes)
 };
@@ -288,7 +288,6 @@ struct MoeLaunch {
   float* weight;  // of the expert of each rank
   int* found;     // experts of each of the n tokens, or -1 for one whose output is NaN
   MoeSlot* slot;  // at most n * top
-  int* active;    // slots with an expert
   void* out;
   hipStream_t stream;
 };

@@ -87,7 +87,6 @@ struct SlotSearch {
       if (w < tid >> 5) before += in_w;
       total += in_w;
     }
-    if (blockIdx.x == 0 && s == 0 && tid == 0) *a.active = total;
     if (s >= total) return -1;
     if (tid < kMoeMaxExperts) {
       const uint32_t word = sh.used[tid >> 5];
@@ -156,13 +155,17 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
   SlotSearch search{a, shared};
   MoeSlot& slot = a.slot[blockIdx.y];
   int e, count;
+  uint16_t entry = 0;
   if constexpr (kGated) {
     e = search.find(blockIdx.y);
-    if (e < 0) return;
+    if (e < 0) {
+      if (blockIdx.x == 0 && tid == 0) slot.expert = -1;
+      return;
+    }
   } else {
-    if (static_cast<int>(blockIdx.y) >= *a.active) return;
     e = slot.expert, count = slot.count;
-    if (tid < count) entries[tid] = slot.entry[tid];
+    if (e < 0) return;
+    if (wave == 0) entry = slot.entry[lane];  // (those behind the last hold anything)
   }
   // Both strips of a tile's rows, in windows of the expert's matrices.
   const int64_t first = static_cast<int64_t>(e) * rows * row_bytes;
@@ -194,6 +197,7 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
       if (tid < count) slot.entry[tid] = entries[tid];
     }
   } else {
+    if (wave == 0) entries[lane] = entry;
     lds_sync();
   }
   for (int t0 = 0; t0 < count; t0 += 16 * T) {
