@@ -272,15 +272,17 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
 // pays as long as the bytes that are read again, for experts taken at random, stay below
 // some 40 MB: with this form and the general one, in us, 6 tokens of top 8 of 64 experts of
 // 2048 x 1024 at 4 bits (47 MB) 42.1 and 47.2, 8 (73 MB) 51.8 and 45.0; 16 of top 3 of 13 of
-// 704 x 448 at 8 bits (34 MB) 18.1 and 20.6, 32 (79 MB) 27.9 and 21.1; 8 of top 4 of 32 of
-// 1024 x 512 at 4 bits (9 MB) 14.7 and 21.9, 16 (28 MB) 24.7 and 22.4.  For up to 4 tokens, where
-// the general form's wide instructions are emptier still, below 100 MB: 4 of top 2 of 8 of
+// 704 x 448 at 8 bits (34 MB) 18.1 and 20.6, 32 (79 MB) 27.9 and 21.1.  A workgroup of gated
+// costs as much as some 32 KB whatever it reads: 12 of top 4 of 32 of 1024 x 512 at 4 bits
+// (so counted 29 MB) 21.2 and 22.0, 16 (44 MB) 24.7 and 22.4.  For up to 4 tokens, where the
+// general form's wide instructions are emptier still, below 100 MB: 4 of top 2 of 8 of
 // 2048 x 5632 at 8 bits (95 MB) 50.4 and 59.8.  LDS holds the codes of a token's h.
 bool moe_is_few(const MoeLaunch& a, bool packed) {
   if (a.n > 32 || a.top * a.m > 1 << 16) return false;
-  const double pairs = a.n * a.top, experts = a.experts;
+  const double pairs = a.n * a.top, experts = a.experts, bytes = 3.0 * a.m * a.k / (packed ? 2 : 1);
   const double chosen = experts * (1.0 - std::pow(1.0 - 1.0 / experts, pairs));
-  return (pairs - chosen) * (3.0 * a.m * a.k) / (packed ? 2 : 1) <= (a.n <= 4 ? 100e6 : 40e6);
+  const double most = a.n <= 4 ? 100e6 : 40e6, each = 32e3 * a.m / 16;
+  return pairs * (bytes > each ? bytes : each) - chosen * bytes <= most;
 }
 
 hipError_t launch_moe_few(const MoeLaunch& a, bool packed, bool out_bf16) {
