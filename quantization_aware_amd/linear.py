@@ -39,7 +39,8 @@ caption).  Both operands are quantised to codes one a byte (quest_quantize_fwd_i
 and the forward product is quest_gemm_i8, with exact sums and one rounding to
 the compute dtype, where the default above 4 bits rounds both operands' values
 to the compute dtype first.  The backward rebuilds them (quest_dequantize_i8) for
-the same two gradient products.  ``freeze`` then keeps the weight's codes.
+the same two gradient products, whose fp32 sums are rounded once, behind the trust
+backward (quest_trust_bwd_narrow).  ``freeze`` then keeps the weight's codes.
 """
 from __future__ import annotations
 
