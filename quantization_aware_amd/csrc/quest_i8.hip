@@ -75,13 +75,15 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Values (2 c + 1) s / (2^b - 1) of 16 codes a thread; cols is a multiple of 64.  Bound
+// Values (2 c + 1) s / (2^b - 1) of 16 codes a thread; cols is a multiple of 64.  At most
+// kDequantChunks of 16 a launch: the index, its division by the row's length and the outputs'
+// 16-byte pieces, up to 4 i + 3, are counted in 32 bits.  Bound
 // by its bytes: 18432 x 2048 to bf16, 113 MB, 20.6 us (5.5 TB/s).
+constexpr int64_t kDequantChunks = int64_t(1) << 30;
 template <typename Out>
 __global__ void __launch_bounds__(256)
-    quest_dequant_i8_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scale, int64_t chunks,
+    quest_dequant_i8_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scale, uint32_t chunks,
                             uint32_t chunks_per_row, float levels, Out* __restrict__ out) {
-  // (fewer than 2^32 chunks: rows * cols stays below 2^36)
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= chunks) return;
   const float c = scale[i / chunks_per_row] / levels;
@@ -179,17 +181,23 @@ hipError_t launch_trust_bwd_narrow(const float* grad, const uint8_t* mask, int64
 
 hipError_t launch_dequantize_i8(const uint8_t* codes, const float* scale, int64_t rows, int64_t cols, int bits,
                                 void* out, int out_is_bf16, hipStream_t stream) {
-  const int64_t chunks = rows * (cols / 16);
-  const dim3 grid(static_cast<uint32_t>((chunks + 255) / 256));
   const float levels = static_cast<float>((1 << bits) - 1);
-  const uint32_t per_row = static_cast<uint32_t>(cols / 16);
-  if (out_is_bf16)
-    hipLaunchKernelGGL((quest_dequant_i8_kernel<uint16_t>), grid, dim3(256), 0, stream, codes, scale, chunks, per_row,
-                       levels, static_cast<uint16_t*>(out));
-  else
-    hipLaunchKernelGGL((quest_dequant_i8_kernel<float>), grid, dim3(256), 0, stream, codes, scale, chunks, per_row,
-                       levels, static_cast<float*>(out));
-  return hipGetLastError();
+  const int64_t per_row = cols / 16, most = kDequantChunks / per_row;  // rows a launch
+  for (int64_t row = 0; row < rows; row += most) {
+    const int64_t chunks = (rows - row < most ? rows - row : most) * per_row;
+    const dim3 grid(static_cast<uint32_t>((chunks + 255) / 256));
+    if (out_is_bf16)
+      hipLaunchKernelGGL((quest_dequant_i8_kernel<uint16_t>), grid, dim3(256), 0, stream, codes + row * cols,
+                         scale + row, static_cast<uint32_t>(chunks), static_cast<uint32_t>(per_row), levels,
+                         static_cast<uint16_t*>(out) + row * cols);
+    else
+      hipLaunchKernelGGL((quest_dequant_i8_kernel<float>), grid, dim3(256), 0, stream, codes + row * cols, scale + row,
+                         static_cast<uint32_t>(chunks), static_cast<uint32_t>(per_row), levels,
+                         static_cast<float*>(out) + row * cols);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace quest
