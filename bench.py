@@ -424,7 +424,7 @@ def qat_linear_step(torch, dev, reps):
     forwards with codes and mask in one grouped launch, the FP6 product; in
     the backward both
     operands rebuilt from their codes in one launch, the two BF16 gradient
-    products, and both gradients masked and transformed back in one launch)
+    products, and each gradient masked and transformed back in place)
     against torch's BF16 linear, each as
     `reps` back-to-back forward + backward passes (torch.autograd.grad, so no
     gradient accumulation) between events on the launch stream, over rotating

@@ -96,8 +96,7 @@ class QuestLinearFunction(torch.autograd.Function):
             # With one bit width and n a multiple of 4 (every buffer 16-byte
             # aligned), the codes, scales and masks of x and w are the rows of
             # one (n + m)-row tensor each, so that the backward rebuilds both
-            # operands in one quest_dequantize launch and masks both gradients
-            # in one quest_trust_bwd launch.
+            # operands in one quest_dequantize launch.
             ctx.joint = bits_x == bits_w and n % 4 == 0
             if ctx.joint:
                 dev = x.device
@@ -171,24 +170,24 @@ class QuestLinearFunction(torch.autograd.Function):
     def _backward_joint(ctx, dy):
         """Both gradients of the FP6 path, x's and w's state held as the rows of one tensor each.
 
-        One rebuild launch gives [Q(x); Q(w)], the two products write
-        [dy Q(w); dy^T Q(x)] (the weight gradient first, while Q(x) is still in
-        the last-level cache), and one trust backward masks and transforms
-        both back in place.
+        One rebuild launch gives [Q(x); Q(w)]; the weight gradient comes first,
+        while Q(x) is still in the last-level cache.  Each gradient is masked
+        and transformed back in a buffer of its own: the weight's outlives the
+        step, and as rows of a joint one would keep the input's with it.
         """
         codes, scale, mask = ctx.saved_tensors
         n, m, k, bits, _, compute_dtype = ctx.dims
         q = dequantize(codes, scale, n + m, k, bits, out_dtype=compute_dtype)
         qx, qw = q[:n], q[n:]
         dy = dy.to(compute_dtype).contiguous()
-        g = torch.empty((n + m, k), dtype=compute_dtype, device=dy.device)
         # gradients reaching Q(w) and Q(x), Hadamard domain (the weight's as a
         # 2-D product with a transposed left operand, as torch's own linear
         # backward computes it)
-        torch.mm(dy.t(), qx, out=g[n:])
-        torch.mm(dy, qw, out=g[:n])
-        trust_bwd(g, mask, ctx.block, out=g)
-        return g[:n].to(ctx.x_dtype), g[n:].to(ctx.w_dtype), None, None, None, None, None, None, None
+        gw = torch.mm(dy.t(), qx)
+        gx = torch.mm(dy, qw)
+        trust_bwd(gw, mask[n:], ctx.block, out=gw)
+        trust_bwd(gx, mask[:n], ctx.block, out=gx)
+        return gx.to(ctx.x_dtype), gw.to(ctx.w_dtype), None, None, None, None, None, None, None
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:

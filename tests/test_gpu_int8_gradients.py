@@ -1,4 +1,4 @@
-"""Gradients of the layers in 8-bit integers: whose memory they hold."""
+"""Gradients of the quantised layers: whose memory they hold."""
 from __future__ import annotations
 
 import pytest
@@ -37,5 +37,16 @@ def test_gradients_hold_their_own_memory(dev, x_dtype, w_dtype, compute, n, bits
     x = torch.randn(n, 256, device=dev).to(x_dtype).requires_grad_()
     w = torch.randn(24, 256, device=dev).to(w_dtype).requires_grad_()
     quest_linear(x, w, bits_x=bits_x, bits_w=bits_w, compute_dtype=compute, int8=True).float().sum().backward()
+    for t in (x, w):
+        assert t.grad.dtype == t.dtype and t.grad.shape == t.shape and owns(t.grad)
+
+
+@pytest.mark.parametrize("x_dtype,w_dtype,compute", TYPES)
+@pytest.mark.parametrize("n", [64, 63])
+def test_gradients_of_the_default_layer_hold_their_own_memory(dev, x_dtype, w_dtype, compute, n):
+    """The same of the FP6 product's layer, whose codes are the rows of one tensor where n is a multiple of 4."""
+    x = torch.randn(n, 256, device=dev).to(x_dtype).requires_grad_()
+    w = torch.randn(24, 256, device=dev).to(w_dtype).requires_grad_()
+    quest_linear(x, w, bits_x=4, bits_w=4, compute_dtype=compute).float().sum().backward()
     for t in (x, w):
         assert t.grad.dtype == t.dtype and t.grad.shape == t.shape and owns(t.grad)
