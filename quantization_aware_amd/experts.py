@@ -116,13 +116,14 @@ class QuestMoE(torch.nn.Module):
         weight, index = route(torch.nn.functional.linear(flat.float(), self.router.float()), self.top_k, self.over_all)
         # (a token's rows: in the order of its experts' index, whatever their rank)
         out = torch.zeros(flat.shape, dtype=torch.float32, device=x.device)
-        for e in range(self.router.shape[0]):
+        # (unbound once: the backward pass of an expert's own select would write zeros for all of the others)
+        for e, (gate_up, down) in enumerate(zip(self.gate_up.unbind(0), self.down.unbind(0))):
             token, rank = torch.nonzero(index == e, as_tuple=True)
             if not token.numel():
                 continue
-            g, u = self._linear(flat[token], self.gate_up[e], self.bits_x).float().chunk(2, -1)
+            g, u = self._linear(flat[token], gate_up, self.bits_x).float().chunk(2, -1)
             h = (torch.nn.functional.silu(g) if self.act == "silu" else torch.nn.functional.gelu(g)) * u
-            y = self._linear(h.to(self.compute_dtype), self.down[e], self.bits_h)
+            y = self._linear(h.to(self.compute_dtype), down, self.bits_h)
             out = out.index_add(0, token, y.float() * weight[token, rank][:, None])
         return out.to(self.compute_dtype).reshape(x.shape)
 
