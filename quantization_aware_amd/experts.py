@@ -12,6 +12,8 @@ sum over the experts, with the weights at 4 bits two in a byte.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import ACTIVATIONS, MOE_MAX_TOKENS, moe_fwd, quantize_fwd, quantize_fwd_i8
@@ -24,11 +26,15 @@ def route(logits: torch.Tensor, top_k: int, over_all: bool = False):
     """(weights, experts) of each token, both (n, top_k), differentiable in the weights.
 
     The top_k largest logits, of equal ones the lowest index; weights are the
-    softmax over them, or with over_all over all logits.
+    softmax over them, or with over_all over all logits.  An expert with a
+    logit of -infinity has the weight 0, also where the token has no other; a
+    NaN or +infinity makes the token's weights NaN.
     """
     value, index = torch.sort(logits.float(), dim=-1, descending=True, stable=True)
+    none = value[:, :1] == -math.inf  # the largest
+    value = value.masked_fill(none, 0.0)
     weight = torch.softmax(value if over_all else value[:, :top_k], dim=-1)[:, :top_k]
-    return weight, index[:, :top_k]
+    return weight.masked_fill(none, 0.0), index[:, :top_k]
 
 
 class QuestMoE(torch.nn.Module):
@@ -113,18 +119,24 @@ class QuestMoE(torch.nn.Module):
             with torch.no_grad():
                 parts = [self._few(_dense(t)) for t in flat.split(MOE_MAX_TOKENS)]
             return (parts[0] if len(parts) == 1 else torch.cat(parts)).reshape(x.shape)
-        weight, index = route(torch.nn.functional.linear(flat.float(), self.router.float()), self.top_k, self.over_all)
+        logits = torch.nn.functional.linear(flat.float(), self.router.float())
+        weight, index = route(logits, self.top_k, self.over_all)
+        index = index.masked_fill(logits.gather(-1, index) == -math.inf, -1)  # not taken
         # (a token's rows: in the order of its experts' index, whatever their rank)
         out = torch.zeros(flat.shape, dtype=torch.float32, device=x.device)
+        taken = False
         # (unbound once: the backward pass of an expert's own select would write zeros for all of the others)
         for e, (gate_up, down) in enumerate(zip(self.gate_up.unbind(0), self.down.unbind(0))):
             token, rank = torch.nonzero(index == e, as_tuple=True)
             if not token.numel():
                 continue
+            taken = True
             g, u = self._linear(flat[token], gate_up, self.bits_x).float().chunk(2, -1)
             h = (torch.nn.functional.silu(g) if self.act == "silu" else torch.nn.functional.gelu(g)) * u
             y = self._linear(h.to(self.compute_dtype), down, self.bits_h)
             out = out.index_add(0, token, y.float() * weight[token, rank][:, None])
+        if not taken:  # zeros, and so are the weights: a backward pass can follow all the same
+            out = out + weight.sum()
         return out.to(self.compute_dtype).reshape(x.shape)
 
     def _few(self, x: torch.Tensor) -> torch.Tensor:

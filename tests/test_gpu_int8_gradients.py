@@ -220,3 +220,28 @@ def check(name, got, want):
     # (the bound is a check at all: a gradient off by a quarter of its size would not pass)
     assert np.linalg.norm(want.err) < 0.25 * np.linalg.norm(want.v), name
     log(f"{name}: {ratio.max():.3g} of the bound, {np.linalg.norm(want.err) / np.linalg.norm(want.v):.2g} of the size")
+
+
+@pytest.mark.parametrize("over_all", [False, True])
+def test_logits_of_minus_infinity(dev, over_all):
+    """Trained and frozen alike: such an expert is not taken, and a token without any gives zeros and no gradient."""
+    torch.manual_seed(4)
+    moe = QuestMoE(128, 64, 4, 2, block=64, bits_x=8, bits_w=8, compute_dtype=torch.float32, over_all=over_all, device=dev)
+    x = torch.randn(5, 128, device=dev)
+    with torch.no_grad():
+        moe.router[:, 0] = torch.tensor([-1e30, -1e30, -1e30, -1e30])
+        moe.router[:, 1] = torch.tensor([0.0, 0.0, 0.0, -1e30])
+        x[:, :2] = 0.0
+        x[1, 0] = 1e10  # every logit -infinity
+        x[3, 1] = 1e10  # that of expert 3
+    x.requires_grad_()
+    y = moe(x)
+    assert (y[1] == 0).all() and y.isfinite().all()
+    y.sum().backward()
+    # (token 3 has y of about 1e18 and so have its logits' gradients: by the router's -1e30 they pass fp32's range)
+    assert x.grad[[0, 1, 2, 4]].isfinite().all() and all(p.grad.isfinite().all() for p in moe.parameters())
+    assert (x.grad[1] == 0).all()
+    frozen = moe.freeze()(x.detach())
+    assert (frozen[1] == 0).all()
+    # (h keeps fp32 on both sides: only codes at a level's edge differ)
+    assert float((frozen - y.detach()).norm() / frozen.norm()) < 0.02
