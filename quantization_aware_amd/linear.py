@@ -328,7 +328,7 @@ def quest_linear_int8(x: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Ten
     cx, sx, _ = quantize_fwd_i8(x2, block, bits_x)
     y = gemm_i8(cx, sx, bits_x, w_codes, w_scale, bits_w, out_dtype=out_dtype)
     if bias is not None:
-        y = y + bias.to(y.dtype)
+        y = y + bias.detach().to(y.dtype)
     return y.reshape(*x.shape[:-1], w_codes.shape[0])
 
 

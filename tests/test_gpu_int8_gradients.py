@@ -11,7 +11,7 @@ import moe_oracle as mo
 import quantization_aware_amd as qa
 from oracle import quest_oracle as qo
 from quantization_aware_amd.experts import QuestMoE, route
-from quantization_aware_amd.linear import quest_linear
+from quantization_aware_amd.linear import QuestLinear, quest_linear, quest_linear_int8
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +245,18 @@ def test_logits_of_minus_infinity(dev, over_all):
     assert (frozen[1] == 0).all()
     # (h keeps fp32 on both sides: only codes at a level's edge differ)
     assert float((frozen - y.detach()).norm() / frozen.norm()) < 0.02
+
+
+# ---------------------------------------------------------------------------
+# The frozen linear layer beside the trained one
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_frozen_outputs_carry_no_gradient(dev, bias, dtype):
+    layer = QuestLinear(256, 96, bias=bias, bits_x=8, bits_w=8, compute_dtype=dtype, int8=True, device=dev).freeze()
+    x = torch.randn(3, 256, device=dev, requires_grad=True)
+    y = layer(x)
+    assert not y.requires_grad and y.grad_fn is None
+    codes, scale = layer._w_operand, layer._w_scale
+    assert not quest_linear_int8(x, codes, scale, 8, bias=layer.bias, out_dtype=dtype).requires_grad
