@@ -322,11 +322,14 @@ def quest_linear_int8(x: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Ten
     """Inference product Q(x) Q(w)^T (+ bias) in 8-bit integers, with w already quantised.
 
     x (..., K) bf16 or fp32; w_codes (M, K) int8 and w_scale (M,) as returned
-    by quantize_fwd_i8 at bits_w.  No gradient flows.
+    by quantize_fwd_i8 at bits_w.  out_dtype: any floating-point type, as
+    quest_linear's compute_dtype.  No gradient flows.
     """
+    if not (isinstance(out_dtype, torch.dtype) and out_dtype.is_floating_point):
+        raise TypeError(f"out_dtype must be a floating-point type, not {out_dtype}")
     x2 = _dense(x.detach().reshape(-1, x.shape[-1]))
     cx, sx, _ = quantize_fwd_i8(x2, block, bits_x)
-    y = gemm_i8(cx, sx, bits_x, w_codes, w_scale, bits_w, out_dtype=out_dtype)
+    y = gemm_i8(cx, sx, bits_x, w_codes, w_scale, bits_w, out_dtype=_product_dtype(out_dtype)).to(out_dtype)
     if bias is not None:
         y = y + bias.detach().to(y.dtype)
     return y.reshape(*x.shape[:-1], w_codes.shape[0])
@@ -389,11 +392,10 @@ class QuestLinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if not self.training and self._w_operand is not None:
-            out_dtype = _product_dtype(self.compute_dtype)
             if self.int8:
                 return quest_linear_int8(x, self._w_operand, self._w_scale, self.bits_w, self.bias, self.block,
-                                         self.bits_x, out_dtype)
+                                         self.bits_x, self.compute_dtype)
             return quest_linear_operand(x, self._w_operand, self._w_scale, self.weight.shape[0], self.bits_w,
-                                        self.bias, self.block, self.bits_x, out_dtype)
+                                        self.bias, self.block, self.bits_x, _product_dtype(self.compute_dtype))
         return quest_linear(x, self.weight, self.bias, self.block, self.bits_x, self.bits_w, self.compute_dtype,
                             self.trust_x, self.trust_w, self.grid, self.int8)

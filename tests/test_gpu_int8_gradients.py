@@ -260,3 +260,16 @@ def test_frozen_outputs_carry_no_gradient(dev, bias, dtype):
     assert not y.requires_grad and y.grad_fn is None
     codes, scale = layer._w_operand, layer._w_scale
     assert not quest_linear_int8(x, codes, scale, 8, bias=layer.bias, out_dtype=dtype).requires_grad
+
+
+@pytest.mark.parametrize("compute", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bias", [True, False])
+def test_frozen_outputs_have_the_trained_type(dev, compute, bias):
+    layer = QuestLinear(256, 96, bias=bias, bits_x=8, bits_w=8, compute_dtype=compute, int8=True, device=dev)
+    if bias:
+        torch.nn.init.normal_(layer.bias)
+    x = torch.randn(3, 5, 256, device=dev)
+    with torch.no_grad():
+        want = layer(x)
+    got = layer.freeze()(x)
+    assert want.dtype == got.dtype == compute and torch.equal(got, want)
