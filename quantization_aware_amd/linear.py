@@ -338,6 +338,8 @@ def quest_linear_int8(x: torch.Tensor, w_codes: torch.Tensor, w_scale: torch.Ten
 class QuestLinear(torch.nn.Module):
     """Drop-in linear layer trained with QuEST quantisation of weights and activations (int8: as in quest_linear)."""
 
+    int8 = False  # (of modules pickled before there was the choice)
+
     def __init__(self, in_features: int, out_features: int, bias: bool = True, block: int = 128, bits_x: int = 4,
                  bits_w: int = 4, compute_dtype=torch.bfloat16, trust_x: float | None = None,
                  trust_w: float | None = None, grid: str = "int", device=None, dtype=None, int8: bool = False):
