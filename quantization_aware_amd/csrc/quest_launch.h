@@ -293,7 +293,7 @@ struct MoeLaunch {
 };
 hipError_t launch_moe(const MoeLaunch& a, bool packed, bool out_bf16);
 // Of it, the form for few tokens, and where it is the faster one.
-bool moe_is_few(const MoeLaunch& a, bool packed);
+bool moe_is_few(int n, int experts, int top, int k, int m, bool packed);
 hipError_t launch_moe_few(const MoeLaunch& a, bool packed, bool out_bf16);
 
 }  // namespace quest

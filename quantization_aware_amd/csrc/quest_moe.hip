@@ -435,7 +435,7 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
 }  // namespace
 
 hipError_t launch_moe(const MoeLaunch& a, bool packed, bool out_bf16) {
-  if (moe_is_few(a, packed)) return launch_moe_few(a, packed, out_bf16);
+  if (moe_is_few(a.n, a.experts, a.top, a.k, a.m, packed)) return launch_moe_few(a, packed, out_bf16);
   return packed ? launch<true>(a, out_bf16) : launch<false>(a, out_bf16);
 }
 

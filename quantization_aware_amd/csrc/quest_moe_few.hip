@@ -269,19 +269,21 @@ hipError_t launch(const MoeLaunch& a, bool out_bf16) {
 
 // This form reads an expert's weights again for each token that takes it, mostly from
 // caches, but spends some 10 us less on launches and what lies between the products.  It
-// pays as long as the bytes that are read again, for experts taken at random, stay below
-// some 40 MB: with this form and the general one, in us, 6 tokens of top 8 of 64 experts of
-// 2048 x 1024 at 4 bits (47 MB) 42.1 and 47.2, 8 (73 MB) 51.8 and 45.0; 16 of top 3 of 13 of
-// 704 x 448 at 8 bits (34 MB) 18.1 and 20.6, 32 (79 MB) 27.9 and 21.1.  A workgroup of gated
-// costs as much as some 32 KB whatever it reads: 12 of top 4 of 32 of 1024 x 512 at 4 bits
-// (so counted 29 MB) 21.2 and 22.0, 16 (44 MB) 24.7 and 22.4.  For up to 4 tokens, where the
-// general form's wide instructions are emptier still, below 100 MB: 4 of top 2 of 8 of
-// 2048 x 5632 at 8 bits (95 MB) 50.4 and 59.8.  LDS holds the codes of a token's h.
-bool moe_is_few(const MoeLaunch& a, bool packed) {
-  if (a.n > 32 || a.top * a.m > 1 << 16) return false;
-  const double pairs = a.n * a.top, experts = a.experts, bytes = 3.0 * a.m * a.k / (packed ? 2 : 1);
-  const double chosen = experts * (1.0 - std::pow(1.0 - 1.0 / experts, pairs));
-  const double most = a.n <= 4 ? 100e6 : 40e6, each = 32e3 * a.m / 16;
+// pays as long as the bytes that are read again, with top of the experts taken by each
+// token at random, stay below some 42 MB: with this form and the general one, in us, 6
+// tokens of top 8 of 64 experts of 2048 x 1024 at 4 bits (40.0 MB) 42.0 and 47.5, 8 (69 MB)
+// 52.1 and 45.1; 16 of top 3 of 13 of 704 x 448 at 8 bits (33 MB) 17.9 and 20.9, 24 (56 MB)
+// 23.6 and 20.7.  A workgroup of gated costs as much as some 32 KB whatever it reads: 12 of
+// top 4 of 32 of 1024 x 512 at 4 bits (so counted 29 MB) 21.8 and 22.9, 16 (43 MB) 24.9 and
+// 22.5.  For up to 4 tokens, where the general form's wide instructions are emptier still,
+// below 100 MB: 4 of top 2 of 8 of 2048 x 5632 at 8 bits (88 MB) 50.6 and 57.4, 2 of top 4
+// of 4 of 4096 x 7168 (352 MB) 137.5 and 85.3.  One token reads nothing again: of top 4 of
+// those 78.6 and 85.0.  LDS holds the codes of a token's h.
+bool moe_is_few(int n, int experts, int top, int k, int m, bool packed) {
+  if (n > 32 || top * m > 1 << 16) return false;
+  const double pairs = n * top, bytes = 3.0 * m * k / (packed ? 2 : 1);
+  const double chosen = experts * (1.0 - std::pow(1.0 - double(top) / experts, n));
+  const double most = n <= 4 ? 100e6 : 42e6, each = 32e3 * m / 16;
   return pairs * (bytes > each ? bytes : each) - chosen * bytes <= most;
 }
 
