@@ -382,20 +382,28 @@ hipError_t launch_product(const MoeLaunch& a, int tiles, int chunks) {
 template <bool kPacked, int kMode>
 hipError_t launch_products(const MoeLaunch& a) {
   constexpr bool kGated = kMode != kDown;
-  // Two groups of 16 tokens at once where an expert has more than 10 on average.
+  // Two groups of 16 tokens at once where an expert has more than 10 on average (a layer of 48 or
+  // 64 tokens in us, one group and two: 16 an expert 102.5 and 66.9, 46.6 and 35.7; 12 an
+  // expert 47.1 and 43.8; 8 an expert 55.9 and 52.4, but 37.0 and 41.5, 46.5 and 53.9; 4 an
+  // expert 74.0 and 75.3).
   const bool two = static_cast<int64_t>(a.n) * a.top > 10 * static_cast<int64_t>(a.experts);
   const int tiles = kGated ? a.m / 16 : a.k / 32;
   const int chunks = ((kGated ? a.k : a.m) + kFewChunk<kPacked> - 1) / kFewChunk<kPacked>;
+  // (the sums of 8 waves and two groups would leave no LDS for a round of codes)
   auto run = [&](auto ks) {
     constexpr int KS = decltype(ks)::value;
     return two ? launch_product<kPacked, 2, KS < 8 ? KS : 4, kMode>(a, tiles, chunks)
                : launch_product<kPacked, 1, KS, kMode>(a, tiles, chunks);
   };
-  // As few waves a tile as keep some 16 waves a compute unit busy.
-  const int64_t waves = static_cast<int64_t>(tiles) * a.slots;
-  if (waves >= 4096 || chunks < 2) return run(std::integral_constant<int, 1>{});
-  if (waves >= 2048 || chunks < 4) return run(std::integral_constant<int, 2>{});
-  if (waves >= 1024 || chunks < 8) return run(std::integral_constant<int, 4>{});
+  // As few waves a tile as keep some 16 waves a compute unit busy, each with a chunk.  (A
+  // layer of 64 tokens in us with 1, 2, 4 waves a tile of one product: 24 tiles a unit
+  // 74.6, 72.7, 75.0 and with 8 84.4; 11 a unit 74.2, 67.0, 70.2; 4 a unit 39.4, 34.9, 38.0;
+  // 2 a unit 103.0, 76.7, 66.7; half a tile a unit 84.0, 57.4, 43.6.  Runs of the same
+  // choice differ by up to 2.5.)
+  const int64_t waves = static_cast<int64_t>(tiles) * a.slots, cus = device_cus();
+  if (waves >= 16 * cus || chunks < 2) return run(std::integral_constant<int, 1>{});
+  if (waves >= 8 * cus || chunks < 4) return run(std::integral_constant<int, 2>{});
+  if (waves >= 4 * cus || chunks < 8) return run(std::integral_constant<int, 4>{});
   return run(std::integral_constant<int, 8>{});
 }
 
