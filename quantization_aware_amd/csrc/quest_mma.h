@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "quest_sync.h"
+
 namespace quest {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -74,13 +76,6 @@ template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
   static_assert(N >= 0 && N < 64, "vmcnt field");
   __builtin_amdgcn_s_waitcnt(0x3F70 | (N & 15) | ((N >> 4) << 14));
-}
-
-// A workgroup barrier that waits for this wave's LDS accesses only (a
-// __syncthreads would also wait for every load and store in flight).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
 }
 
 // Tile index -> (tm, tn): groups of 8 tile rows, walked column by column.

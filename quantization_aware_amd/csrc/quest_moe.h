@@ -1,20 +1,12 @@
-// What the kernels of quest_moe_fwd share: a token's choice of experts, the gated
-// product's activation, and a barrier.
+// What the kernels of quest_moe_fwd share: a token's choice of experts and the gated
+// product's activation.
 #pragma once
 
 #include "quest_device.h"
 #include "quest_launch.h"
+#include "quest_sync.h"
 
 namespace quest {
-
-// A workgroup barrier that waits for this wave's LDS accesses only: loads of weights
-// stay in flight across it (a __syncthreads waits for them).
-__device__ __forceinline__ void lds_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // A token's logits as they lie in memory, expert 64 i + lane in raw[i] (past the last:
 // the last again).  Kept apart from their use, so that other loads can follow at once.

@@ -75,11 +75,11 @@ struct SlotSearch {
     }
     if (tid < kMoeMaxExperts / 32) sh.used[tid] = 0;
     if (tid == 0) sh.expert = -1;
-    lds_sync();
+    lds_barrier();
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
       if (mine[j] >= 0) atomicOr(&sh.used[mine[j] >> 5], 1u << (mine[j] & 31));
-    lds_sync();
+    lds_barrier();
     int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
@@ -93,7 +93,7 @@ struct SlotSearch {
       before += __builtin_popcount(word & ((1u << (tid & 31)) - 1));
       if ((word >> (tid & 31) & 1) && before == s) sh.expert = tid;
     }
-    lds_sync();
+    lds_barrier();
     return __builtin_amdgcn_readfirstlane(sh.expert);
   }
 
@@ -105,7 +105,7 @@ struct SlotSearch {
       at[j] = __builtin_amdgcn_ballot_w64(mine[j] == e);
       if (lane == 0) sh.hits[j * kWaves + wave] = __builtin_popcountll(at[j]);
     }
-    lds_sync();
+    lds_barrier();
     int count = 0;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
@@ -122,7 +122,7 @@ struct SlotSearch {
         entries[before] = static_cast<uint16_t>(t | (p - t * a.top) << 8);
       }
     }
-    lds_sync();
+    lds_barrier();
     return count;
   }
 };
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
     }
   } else {
     if (wave == 0) entries[lane] = entry;
-    lds_sync();
+    lds_barrier();
   }
   for (int t0 = 0; t0 < count; t0 += 16 * T) {
     const int here = min(count - t0, 16 * T);
@@ -223,18 +223,18 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
     if (t0 > 0) {
       tile = blockIdx.x * kTiles + wave / KS;
       begin();
-      lds_sync();  // the last group's codes have been read
+      lds_barrier();  // the last group's codes have been read
     }
     stage(0);
-    lds_sync();
+    lds_barrier();
     // (every wave makes the same steps: those without a tile only wait with the others)
     for (int base = blockIdx.x * kTiles; base < tiles; base += stride, tile += stride) {
       FewSums<kPacked, 2, T> s;
       for (int seg = 0; seg < segments; ++seg) {
         if (segments > 1 && (seg > 0 || base != static_cast<int>(blockIdx.x) * kTiles)) {
-          lds_sync();
+          lds_barrier();
           stage(seg);
-          lds_sync();
+          lds_barrier();
         }
         const int last = seg + 1 < segments ? (seg + 1) * (segment / KS) : steps;
         for (int i0 = seg * (segment / KS); i0 < last; i0 += kAhead) {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
 #pragma unroll
           for (int t = 0; t < T; ++t)
             *reinterpret_cast<v4u*>(&part[wave][p][(16 * t + (lane & 15)) * 16 + 4 * g]) = s.total(p, t);
-        lds_sync();
+        lds_barrier();
         // Quads of the step's outputs: tile, (down: strip,) token, 4 columns.
         constexpr int kStrips = kGated ? 1 : 2;
         for (int o = tid; o < kTiles * kStrips * T * 64; o += 64 * kWaves) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(64 * kWaves) quest_moe_product_kernel(const Mo
           }
           finish(p, i, base + of, 4 * (q % 4), sum0, sum1);
         }
-        lds_sync();
+        lds_barrier();
       }
     }
   }

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves) quest_moe_few_gated_kernel(c
       if (lane == 0) a.found[t] = choice.found;
     }
   }
-  lds_sync();
+  lds_barrier();
   const int expert = __builtin_amdgcn_readfirstlane(shared_expert);
   if (expert < 0) return;
   const int64_t row0 = static_cast<int64_t>(expert) * a.m + col0;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves) quest_moe_few_gated_kernel(c
   if ((lane & 15) == 0)
 #pragma unroll
     for (int p = 0; p < 2; ++p) *reinterpret_cast<v4u*>(&part[wave][p][4 * g]) = s.total(p, 0);
-  lds_sync();
+  lds_barrier();
   if (tid >= 16) return;
   uint32_t sum[2];
 #pragma unroll
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(64 * kDownWaves)
   for (int r0 = 0; r0 < a.top; r0 += at_once) {
     const int row = r0 + lrow;
     const bool works = wave * 64 < min(at_once, a.top - r0) * runs, active = lrow < at_once && row < a.top;
-    if (r0 > 0 && per_row > 1) lds_sync();  // the last rows' sums have been read
+    if (r0 > 0 && per_row > 1) lds_barrier();  // the last rows' sums have been read
     uint32_t raw[RUN];
     if (works) {
       const u32x4* const src = reinterpret_cast<const u32x4*>(
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(64 * kDownWaves)
       if (per_row > 1 && (tid & ((1 << log_group) - 1)) == 0) part[tid >> log_group] = ss;
     }
     if (per_row > 1) {
-      lds_sync();
+      lds_barrier();
       ss = 0.0f;
       if (active)
         for (int i = 0; i < per_row; ++i) ss += part[lrow * per_row + i];
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(64 * kDownWaves)
     if (tid < 16) store(found < 0 ? __builtin_nanf("") : 0.0f);
     return;
   }
-  lds_sync();
+  lds_barrier();
   for (; rank < found; rank += each) {
     if (rank >= each) begin();
     FewSums<kPacked, 1, 1> s;
@@ -219,13 +219,13 @@ __global__ void __launch_bounds__(64 * kDownWaves)
     });
     if ((lane & 15) == 0) *reinterpret_cast<v4u*>(&sums[(rank << log_ks) + ks][4 * g]) = s.total(0, 0);
   }
-  lds_sync();
+  lds_barrier();
   if (tid < 16 * found) {
     uint32_t sum = few_constant<kPacked>(m);
     for (int i = 0; i < 1 << log_ks; ++i) sum += sums[(of << log_ks) + i][tid & 15];
     prod[of][tid & 15] = (static_cast<float>(static_cast<int>(sum)) * 0.25f) * ((clip[of] * a.kh) * fd);
   }
-  lds_sync();
+  lds_barrier();
   if (tid >= 16) return;
   float y = 0.0f;
   for (int r = 0; r < found; ++r) y = fmaf(weight[r], prod[r][tid], y);
