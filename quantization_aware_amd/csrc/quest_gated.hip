@@ -85,6 +85,20 @@ __device__ __forceinline__ void act_both(float g, int act, float& value, float& 
   }
 }
 
+// 16 bytes of LDS to a row's `left` last elements of T at any multiple of T's
+// size: in one store, or the row's last few one by one.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* dst, const uint8_t* src, int left) {
+  typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(1)));
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  if (left >= kPer) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(src);
+    *reinterpret_cast<u32x4_u*>(dst) = v;
+  } else {
+    for (int e = 0; e < left; ++e) dst[e] = reinterpret_cast<const T*>(src)[e];
+  }
+}
+
 template <typename Out, int kB>
 constexpr int kSlabPitch = 32 * kB * static_cast<int>(sizeof(Out)) + 16;  // bytes of a slab's row, 32 rows a slab
 
