@@ -13,16 +13,19 @@
 // |T| < 2^24 both products give the same bits.
 //
 // Large products are bound by the matrix cores, and there by power: 16384 x 2048 -> 5632
-// takes 200 to 216 us, 1.75 to 1.9 POP/s (a library's product of the same codes to int32,
-// without scales, 215; instructions alone on such data 3.5 POP/s, on zeros 4.5).  What is
-// between: writing the 185 MB of outputs (some 50 us of it without the epilogue), the
+// takes 205 to 215 us back to back, 1.75 to 1.85 POP/s (a library's product of the same
+// codes to int32, without scales, 215; instructions alone on such data 3.5 POP/s, on zeros
+// 4.5).  What is between: writing the 185 MB of outputs (some 50 us of it without the epilogue), the
 // loads (40 without them) and the row sums (2 to 12).  Sums by dot products after the
 // four products of a part, not between them: there they stall the matrix cores (+ 26 us).
 // Outputs written through the L2 (sc0 sc1) leave it to the operands: 17 us less than
 // plain stores; non-temporal ones gain 14 here and lose 9 at 16384 x 2048 -> 2048.
-// 2048 x 5632 -> 2048 takes 30.4 us (its 256 tiles read 12 TB/s from the L2; 4 waves of
-// 64 x 64 each instead of 8, or three stages, change nothing), 4096 x 2048 -> 5632 54, 333 x 960 -> 1001 to fp32 4.7,
-// 48 x 2048 -> 5632 6.5 and one row 2048 -> 2048 3.1 us: the last three are latency.
+// 2048 x 5632 -> 2048 takes 30.2 us (its 256 tiles read 12 TB/s from the L2; 4 waves of
+// 64 x 64 each instead of 8, or three stages, change nothing), 4096 x 2048 -> 5632 58, 333
+// x 960 -> 1001 to fp32 5.8, 48 x 2048 -> 5632 7.3 and one row 2048 -> 2048 3.9 us (medians
+// of a kernel trace).  The last is latency.  At 17 to 128 rows each workgroup takes all
+// stages of k, and narrow outputs leave compute units without one: 48 x 2048 -> 5632 is 88
+// workgroups of 16 stages, for 2.5 us of bytes.
 #include <type_traits>
 
 #include "quest_few.h"
@@ -415,8 +418,8 @@ float cost(const GemmI8Launch& g, const Variant& v, int cus) {
 template <typename Out, bool kVec>
 hipError_t launch(const GemmI8Launch& g) {
   const int cus = device_cus();
-  // Few rows of one operand and not too many bytes of the other: 1 x 2048 -> 2048 takes 3.1 us (6.1 in 64 x 64
-  // tiles), 16 x 2048 -> 5632 5.8 (6.3), but 16 x 8192 -> 8192 16.9 (16.2) and 32 rows 7.7 (6.4).
+  // Few rows of one operand and not too many bytes of the other: 1 x 2048 -> 2048 takes 3.9 us (6.9 in 64 x 64
+  // tiles), 5 x 5632 -> 2048 6.7 (12.6), 16 x 2048 -> 5632 7.4 (7.2), 16 x 8192 -> 8192 18.2 (17.8).
   constexpr int64_t kFewBytes = int64_t(1) << 25;
   if (g.m <= 16 && static_cast<int64_t>(g.n) * g.k <= kFewBytes) {
     hipLaunchKernelGGL((quest_gemm_i8_few_kernel<Out, false>), dim3((g.n + 15) / 16), dim3(512), 0, g.stream, g);

@@ -18,7 +18,7 @@ extern __shared__ u32x4 i8_lds[];
 
 // A workgroup holds rows_per_wg whole rows, a lane a run of 32 entries, as in
 // quest_fwd_rows_kernel; rows within a wave need no LDS for their sums.  Bound by its
-// bytes: 16384 x 2048 bf16 with the mask, 105 MB, 22.4 us (4.7 TB/s, a copy's 4.84).
+// bytes: 16384 x 2048 bf16 with the mask, 105 MB, 22.5 us (4.7 TB/s, a copy's 4.84).
 template <typename In, int LOGN>
 __global__ void __launch_bounds__(1024)
     quest_fwd_i8_kernel(const In* __restrict__ x, int64_t rows, int runs_per_row, int rows_per_wg, int log_group,
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(1024)
 
 // Values (2 c + 1) s / (2^b - 1) of 16 codes a thread; cols is a multiple of 64.  At most
 // kDequantChunks of 16 a launch: the index, its division by the row's length and the outputs'
-// 16-byte pieces, up to 4 i + 3, are counted in 32 bits.  Bound
-// by its bytes: 18432 x 2048 to bf16, 113 MB, 20.6 us (5.5 TB/s).
+// 16-byte pieces, up to 4 i + 3, are counted in 32 bits.  Bound by its bytes: 18432 x 2048
+// to bf16, 113 MB, 20.7 us (5.5 TB/s).
 constexpr int64_t kDequantChunks = int64_t(1) << 30;
 template <typename Out>
 __global__ void __launch_bounds__(256)
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // quest_bwd_kernel with fp32 gradients in and bf16 out: the gradients of products in
-// 8-bit integers are rounded once.  Bound by its bytes: 18432 x 2048, 226 MB, 39.4 us (5.8 TB/s).
+// 8-bit integers are rounded once.  Bound by its bytes: 18432 x 2048, 231 MB, 37.1 us (6.2 TB/s).
 template <int LOGN>
 __global__ void __launch_bounds__(256)
     quest_bwd_narrow_kernel(const float* __restrict__ grad, const uint32_t* __restrict__ mask, int64_t total_runs,
@@ -139,8 +139,9 @@ hipError_t launch_fwd(const In* x, int bits, const FwdLaunch& a) {
   if (rows_per_wg * runs > 1024) rows_per_wg = 1024 / runs;
   if (rows_per_wg < 1) rows_per_wg = 1;
   while (rows_per_wg * runs <= 128) rows_per_wg *= 2;
-  // Few rows are spread over the compute units, since their time is a workgroup's (5 x 5632
-  // in fp32 in 2 workgroups of 11 waves 4.4 us, in 5 of 3 waves 3.1; 700 x 960 5.2 and 3.5).
+  // Few rows are spread over the compute units, since their time is a workgroup's (in one
+  // kernel trace, 5 x 5632 in fp32 in 2 workgroups of 11 waves 4.8 us, in 5 of 3 waves 3.8;
+  // 700 x 960 5.8 and 4.0).
   const int64_t spread = a.rows / (2 * device_cus());
   if (rows_per_wg > spread) rows_per_wg = spread < 1 ? 1 : static_cast<int>(spread);
   const int threads = ((rows_per_wg * runs + 63) / 64) * 64;

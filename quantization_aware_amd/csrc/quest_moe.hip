@@ -22,9 +22,9 @@
 // No atomics on results: the sums' order is fixed.  The workspace need not be set.
 //
 // What bounds it is reading the weights: 64 tokens of top 8 of 128 experts of 2048 x 768 at
-// 4 bits, 302 MB, take 42.8 us in gated and 24.6 in down, 4.7 and 4.1 TB/s (a copy of 2 GiB
-// reaches 4.84); of 8 experts of 2048 x 5632 at 8 bits, 277 MB, 44.4 and 24.3 (4.2 and
-// 3.8).  That needs every load issued without a branch around it: with one, each wait was
+// 4 bits, 302 MB, take 43.0 us in gated and 24.5 in down, 4.7 and 4.1 TB/s (a copy of 2 GiB
+// reaches 4.84); of 8 experts of 2048 x 5632 at 8 bits, 277 MB, 40.6 and 22.2 (4.5 and
+// 4.2; in other runs up to 44.4 and 24.5).  That needs every load issued without a branch around it: with one, each wait was
 // for all loads on their way, 50 and 26 us, 54 and 28.5.  The other three kernels are some
 // 5 us each.
 #include <type_traits>

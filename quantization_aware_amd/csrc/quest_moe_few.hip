@@ -13,7 +13,7 @@
 // results are the same bits.
 //
 // What bounds it is latency: one token of top 8 of 64 experts of 2048 x 1024 at 4 bits
-// takes 8.1 + 8.0 us (the general form's five kernels 25.2), of which its 25 MB are 5.2 at
+// takes 8.2 + 8.7 us (the general form's five kernels 25.2), of which its 25 MB are 5.2 at
 // a copy's rate; two launches, the logits and then the weights behind them, and h and
 // then its transform are the rest.  Measured against it: all waves looking for the expert
 // themselves 17.5 together, 8 waves in gated 15.7 (but 33.4 instead of 30.8 for three

@@ -245,7 +245,7 @@ class QuestLinearInt8Function(torch.autograd.Function):
             return trust_bwd_narrow(g, mask, block) if to == torch.bfloat16 else trust_bwd(g, mask, block, out=g)
 
         # The products' sums stay in fp32 up to the gradients' own type: rounded to bf16 both before and after the
-        # transform, and Q before the product, the gradients were 0.0029 off instead of 0.0024 (a rounding is 0.0017).
+        # transform, and Q before the product, the gradients were 0.0029 off instead of 0.0023 (a rounding is 0.0017).
         # Each gradient has a buffer of its own: the weight's is kept behind the step, and as rows of a joint one it
         # would keep the input's rows as well (151 MB for 16.8 MB at 16384 x 2048 -> 2048 in fp32).
         if ctx.joint and need_x and need_w:
@@ -304,7 +304,7 @@ def quest_linear_operand(x: torch.Tensor, w_operand: torch.Tensor, w_scale: torc
     x (..., K) bf16 or fp32 with K a multiple of 128; w_operand / w_scale as
     returned by quantize_fwd_op for the (out_features x K) weight at bits_w.
     The activation is quantised (b = bits_x <= 4) straight into its operand
-    and multiplied on the matrix cores; no gradient flows.
+    and multiplied on the matrix cores; no gradient flows but the bias's.
     """
     lead = x.shape[:-1]
     k = x.shape[-1]
