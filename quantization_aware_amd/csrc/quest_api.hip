@@ -170,8 +170,8 @@ quest_status check_spans(const Span* s, int count) {
   return QUEST_OK;
 }
 
-// rows * cols must stay below 2^36 so that the number of 32-element runs fits
-// in 31 bits.
+// rows * cols is at most 2^36: no more than 2^31 runs of 32 elements, whose
+// work-items, padded to whole workgroups, fit 32 bits.
 constexpr int64_t kMaxElements = int64_t(1) << 36;
 constexpr int64_t kMaxAct8Cols = int64_t(1) << 20;
 
